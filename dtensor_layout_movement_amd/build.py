@@ -16,10 +16,12 @@ REPO_DIR = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(REPO_DIR, "include")
 LIB_PATH = os.path.join(PKG_DIR, "libreshard.so")
-SOURCES = [os.path.join(CSRC, "plan.cpp"), os.path.join(CSRC, "kernel.hip"), os.path.join(CSRC, "reshard.hip")]
+SOURCES = [os.path.join(CSRC, f) for f in ("plan.cpp", "kernel.hip", "reshard.hip", "blocks.hip",
+                                           "block_quantize.hip", "block_matmul.hip", "block_grad.hip")]
 
-# Packed-fp32 instructions are kept out of every HIP object; the library does no
-# floating point, so this costs nothing.
+# Packed-fp32 instructions are kept out of every HIP object; the copy kernel does
+# no floating point and the block-scaled products do theirs on the matrix cores,
+# so this costs nothing.
 HIP_FLAGS = [
     "-O3", "-std=c++17", "-fPIC", "-Wall",
     "--offload-arch=gfx950",
@@ -35,7 +37,7 @@ def hipcc() -> str:
 
 
 def build(verbose: bool = False) -> str:
-    """Compile plan.cpp + kernel.hip + reshard.hip into libreshard.so; return its path."""
+    """Compile SOURCES into libreshard.so; return its path."""
     tmp = LIB_PATH + ".tmp"
     cmd = [hipcc(), *HIP_FLAGS, "-shared", "-I", INCLUDE, "-I", CSRC, *SOURCES, "-o", tmp]
     if verbose:

@@ -1,0 +1,133 @@
+// Device helpers of the block-scaled kernels: float formats, scale bytes and
+// vector types.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "reshard.h"
+
+namespace rs {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// Element types by their dtype code.
+template <int DT> struct Elem;
+template <> struct Elem<RESHARD_DTYPE_F32> {
+  typedef float type;
+  static __device__ float up(float x) { return x; }
+  static __device__ float down(float x) { return x; }
+};
+template <> struct Elem<RESHARD_DTYPE_BF16> {
+  typedef __bf16 type;
+  static __device__ float up(__bf16 x) { return float(x); }
+  static __device__ __bf16 down(float x) { return __bf16(x); }  // to nearest, ties to even
+};
+template <> struct Elem<RESHARD_DTYPE_F16> {
+  typedef _Float16 type;
+  static __device__ float up(_Float16 x) { return float(x); }
+  static __device__ _Float16 down(float x) { return _Float16(x); }
+};
+
+// N elements from or to any address aligned to one element (gfx950 global
+// accesses need no alignment: one wide access each).
+template <typename T, int N> struct Pack {
+  T v[N];
+};
+template <typename T, int N> __device__ __forceinline__ Pack<T, N> load_pack(const T* p) {
+  Pack<T, N> r;
+  __builtin_memcpy(&r, p, sizeof(r));
+  return r;
+}
+template <typename T, int N> __device__ __forceinline__ void store_pack(T* p, const Pack<T, N>& r) {
+  __builtin_memcpy(p, &r, sizeof(r));
+}
+
+// 2^(b - 127) of a scale byte (255: NaN, 0: the subnormal 2^-127).
+__device__ __forceinline__ float scale_value(uint32_t b) {
+  const uint32_t bits = b == 0 ? 0x00400000u : b == 255 ? 0x7fc00000u : b << 23;
+  return __builtin_bit_cast(float, bits);
+}
+
+// The bits of |x| where x is finite, else 0: as unsigned integers they order as
+// the magnitudes do.
+__device__ __forceinline__ uint32_t finite_magnitude(float x) {
+  const uint32_t m = __builtin_bit_cast(uint32_t, x) & 0x7fffffffu;
+  return m < 0x7f800000u ? m : 0u;
+}
+
+// The scale byte of a block whose largest finite magnitude has bits `amax`.  The
+// format's largest value is 1.75 * 2^t (t = 8 for E4M3, 15 for E5M2), so with
+// amax = m * 2^x, 1 <= m < 2, the exponent is x - t, one more where m > 1.75,
+// and at least -127.
+template <bool E5M2> __device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
+  if (amax == 0) return 127;
+  const int e = int(amax >> 23) - (E5M2 ? 15 : 8) + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return uint32_t(max(e, 0));
+}
+
+// 2^(127 - b), the inverse of a scale that scale_byte gave (b <= 247: a normal
+// number), by which an element is multiplied exactly before it is rounded.
+__device__ __forceinline__ float inverse_scale(uint32_t b) {
+  return __builtin_bit_cast(float, (254u - b) << 23);
+}
+
+// Four elements times `inv`, rounded to 8 bits; what is not finite becomes NaN
+// (E5M2 has infinities, which the conversion would give).
+template <bool E5M2> __device__ __forceinline__ uint32_t quantize4(float a, float b, float c, float d, float inv) {
+  if (E5M2) {
+    const auto nan = [](float x) {
+      return (__builtin_bit_cast(uint32_t, x) & 0x7fffffffu) < 0x7f800000u ? x : __builtin_nanf("");
+    };
+    a = nan(a), b = nan(b), c = nan(c), d = nan(d);
+    int r = __builtin_amdgcn_cvt_pk_bf8_f32(a * inv, b * inv, 0, false);
+    return uint32_t(__builtin_amdgcn_cvt_pk_bf8_f32(c * inv, d * inv, r, true));
+  }
+  int r = __builtin_amdgcn_cvt_pk_fp8_f32(a * inv, b * inv, 0, false);
+  return uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(c * inv, d * inv, r, true));
+}
+
+// Four 8-bit elements as binary32 (exact).
+template <bool E5M2> __device__ __forceinline__ f32x4 widen4(uint32_t q) {
+  f32x4 r;
+  if (E5M2) {
+    r[0] = __builtin_amdgcn_cvt_f32_bf8(int(q), 0);
+    r[1] = __builtin_amdgcn_cvt_f32_bf8(int(q), 1);
+    r[2] = __builtin_amdgcn_cvt_f32_bf8(int(q), 2);
+    r[3] = __builtin_amdgcn_cvt_f32_bf8(int(q), 3);
+  } else {
+    r[0] = __builtin_amdgcn_cvt_f32_fp8(int(q), 0);
+    r[1] = __builtin_amdgcn_cvt_f32_fp8(int(q), 1);
+    r[2] = __builtin_amdgcn_cvt_f32_fp8(int(q), 2);
+    r[3] = __builtin_amdgcn_cvt_f32_fp8(int(q), 3);
+  }
+  return r;
+}
+
+// Eight 8-bit elements times a power of two as bfloat16: exact while the value
+// stays in bfloat16's normal range (three significant bits and the hidden one).
+template <bool E5M2> __device__ __forceinline__ bf16x8 widen8_bf16(uint32_t lo, uint32_t hi, float scale) {
+  bf16x2 p[4];
+  if (E5M2) {
+    p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, scale, false);
+    p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, scale, true);
+    p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, scale, false);
+    p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, scale, true);
+  } else {
+    p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
+    p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
+    p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
+    p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
+  }
+  bf16x8 r;
+  __builtin_memcpy(&r, p, sizeof(r));
+  return r;
+}
+
+}  // namespace rs

@@ -1,0 +1,51 @@
+// Block-scaled 8-bit matrices: the launch interface of their kernels
+// (block_quantize.hip, block_matmul.hip, block_grad.hip), used by the host code
+// of the C ABI (blocks.hip).  The callers have checked every matrix.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+#include <string>
+
+#include "reshard.h"
+
+namespace rs {
+
+// Keeps `msg` as the calling thread's last error and returns `s` (reshard.hip).
+reshard_status_t report(reshard_status_t s, const std::string& msg);
+
+constexpr int kBlock = RESHARD_BLOCK;
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+inline int64_t blocks_of(int64_t cols) { return ceil_div(cols, kBlock); }
+
+// Workgroups of one launch at most: a dispatch counts its work-items in 32 bits
+// (512 of them in the largest workgroup used here).
+constexpr int64_t kMaxGroups = (int64_t(1) << 23) - 1;
+
+hipError_t launch_quantize(const reshard_matrix_t& src, const reshard_matrix_t& dst, const reshard_matrix_t* dst_t,
+                           hipStream_t stream);
+hipError_t launch_dequantize(const reshard_matrix_t& src, const reshard_matrix_t& dst, hipStream_t stream);
+
+// How a product runs: workspace bytes and launches.
+struct MatmulPlan {
+  int64_t groups = 0;        // workgroups of the product
+  int64_t quantized = 0;     // bytes of a's quantized payload in the workspace (0: not needed)
+  int64_t quantized_scales = 0;
+  int64_t bytes() const { return quantized + quantized_scales; }
+};
+MatmulPlan plan_matmul(const reshard_matrix_t& a, const reshard_matrix_t& b, const reshard_matrix_t& out);
+hipError_t launch_matmul(const MatmulPlan& plan, const reshard_matrix_t& a, const reshard_matrix_t& b,
+                         const reshard_matrix_t& out, void* workspace, hipStream_t stream);
+
+struct GradPlan {
+  int64_t groups = 0;
+  int64_t bytes() const { return 0; }
+};
+GradPlan plan_grad(const reshard_matrix_t& dy, const reshard_matrix_t& x, const reshard_matrix_t& dw);
+hipError_t launch_grad(const GradPlan& plan, const reshard_matrix_t& dy, const reshard_matrix_t& x,
+                       const reshard_matrix_t& dw, bool accumulate, void* workspace, hipStream_t stream);
+
+}  // namespace rs

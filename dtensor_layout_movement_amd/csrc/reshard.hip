@@ -10,6 +10,7 @@
 #include <string>
 #include <vector>
 
+#include "blocks.h"
 #include "kernel.h"
 #include "plan.h"
 #include "reshard.h"
@@ -37,6 +38,8 @@ reshard_status_t hip_fail(hipError_t e, const char* what) {
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 }  // namespace
+
+reshard_status_t rs::report(reshard_status_t s, const std::string& msg) { return fail(s, msg); }
 
 // ------------------------------------------------------------------ host side
 

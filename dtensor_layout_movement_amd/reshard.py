@@ -58,6 +58,8 @@ EXPORTED = (
     "reshard_plan_device_refs", "reshard_plan_device_segments",
     "reshard_plan_piece_fanout",
     "reshard_plan_descriptors", "reshard_plan_segments", "reshard_plan_destroy",
+    "reshard_block_quantize", "reshard_block_dequantize", "reshard_block_matmul",
+    "reshard_block_matmul_workspace", "reshard_block_grad", "reshard_block_grad_workspace",
     "reshard_last_error",
 )
 
@@ -103,10 +105,22 @@ class Segment(ctypes.Structure):
 
 assert ctypes.sizeof(Segment) == 32
 
+BLOCK = 128  # columns of a scale block
+
+
+class Matrix(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("block_rows", ctypes.c_int32), ("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64),
+                ("scales", ctypes.c_void_p), ("scale_stride", ctypes.c_int64)]
+
+
+assert ctypes.sizeof(Matrix) == 56
+
 _lib = None
 _VP = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I64P = ctypes.POINTER(ctypes.c_int64)
+_MATP = ctypes.POINTER(Matrix)
 
 
 def library_path() -> str:
@@ -150,6 +164,12 @@ def _load() -> ctypes.CDLL:
                                           ctypes.POINTER(ctypes.c_uint32), _I64P]),
         "reshard_plan_segments": (st, [_VP, _I64, ctypes.POINTER(Segment), _I64P]),
         "reshard_plan_destroy": (None, [_VP]),
+        "reshard_block_quantize": (st, [_MATP, _MATP, _MATP, _VP]),
+        "reshard_block_dequantize": (st, [_MATP, _MATP, _VP]),
+        "reshard_block_matmul": (st, [_MATP, _MATP, _MATP, _VP, _I64, _VP]),
+        "reshard_block_matmul_workspace": (st, [_MATP, _MATP, _MATP, _I64P]),
+        "reshard_block_grad": (st, [_MATP, _MATP, _MATP, ctypes.c_int, _VP, _I64, _VP]),
+        "reshard_block_grad_workspace": (st, [_MATP, _MATP, _MATP, _I64P]),
         "reshard_last_error": (ctypes.c_char_p, []),
     }
     for name, (res, args) in sig.items():
@@ -393,6 +413,57 @@ def reshard_plan_segments(plan: int) -> list[dict]:
 
 def reshard_plan_destroy(plan: int) -> None:
     _load().reshard_plan_destroy(plan)
+
+
+def matrix(rows: int, cols: int, dtype: int, data: int | None, row_stride: int | None = None, block_rows: int = 0,
+           scales: int | None = None, scale_stride: int | None = None) -> Matrix:
+    """Describe a matrix in device memory for the block-scaled calls (reusable
+    across calls; the memory stays the caller's).  ``block_rows`` 0: a plain
+    F32, BF16 or F16 matrix; 1 or 128: an FP8 payload with ``scales``.  Strides
+    default to the smallest that the format allows."""
+    blocks = -(-int(cols) // BLOCK)
+    if row_stride is None:
+        row_stride = blocks * BLOCK if block_rows else cols
+    if scale_stride is None:
+        scale_stride = blocks if block_rows else 0
+    return Matrix(int(rows), int(cols), int(dtype), int(block_rows), data or None, int(row_stride), scales or None,
+                  int(scale_stride))
+
+
+def reshard_block_quantize(src: Matrix, dst: Matrix, dst_t: Matrix | None = None, stream: int | None = None) -> None:
+    """Quantize ``src`` into ``dst`` and, when given, its transpose into ``dst_t``."""
+    _check(_load().reshard_block_quantize(src, dst, dst_t, stream or None))
+
+
+def reshard_block_dequantize(src: Matrix, dst: Matrix, stream: int | None = None) -> None:
+    _check(_load().reshard_block_dequantize(src, dst, stream or None))
+
+
+def reshard_block_matmul_workspace(a: Matrix, b: Matrix, out: Matrix) -> int:
+    """Bytes of device workspace that reshard_block_matmul needs."""
+    n = ctypes.c_int64()
+    _check(_load().reshard_block_matmul_workspace(a, b, out, ctypes.byref(n)))
+    return n.value
+
+
+def reshard_block_matmul(a: Matrix, b: Matrix, out: Matrix, workspace: int | None = None, workspace_bytes: int = 0,
+                         stream: int | None = None) -> None:
+    """out[m, n] = sum of a[m, k] * b[n, k]; a plain ``a`` is quantized on the way."""
+    _check(_load().reshard_block_matmul(a, b, out, workspace or None, int(workspace_bytes), stream or None))
+
+
+def reshard_block_grad_workspace(dy: Matrix, x: Matrix, dw: Matrix) -> int:
+    """Bytes of device workspace that reshard_block_grad needs."""
+    n = ctypes.c_int64()
+    _check(_load().reshard_block_grad_workspace(dy, x, dw, ctypes.byref(n)))
+    return n.value
+
+
+def reshard_block_grad(dy: Matrix, x: Matrix, dw: Matrix, accumulate: bool = False, workspace: int | None = None,
+                       workspace_bytes: int = 0, stream: int | None = None) -> None:
+    """dw[n, k] (+)= sum of dy[m, n] * x[m, k] from the 8-bit checkpoint ``x``."""
+    _check(_load().reshard_block_grad(dy, x, dw, int(bool(accumulate)), workspace or None, int(workspace_bytes),
+                                      stream or None))
 
 
 def reshard_last_error() -> str:

@@ -515,6 +515,112 @@ reshard_status_t reshard_plan_segments(reshard_plan_t plan, int64_t capacity,
 /* Free the plan and its device memory.  No execute using it may be in flight.  NULL is a no-op. */
 void reshard_plan_destroy(reshard_plan_t plan);
 
+/*
+ * Block-scaled 8-bit matrices: what a refit to an 8-bit inference layout puts in
+ * place of a 16- or 32-bit weight, what a trainer keeps of an activation for the
+ * backward pass, and the products that use them.
+ *
+ * Format.  A block-scaled matrix holds one 8-bit float (FP8_E4M3 or FP8_E5M2)
+ * per element and one scale byte b per block of 128 columns and `block_rows`
+ * rows (1: activations and gradients, 128: weights; the last blocks of a side
+ * may be short).  The element stands for q * 2^(b - 127); b = 255 is NaN.
+ * Scales are powers of two, so that reading an element back is exact, writing
+ * one rounds once, and the scaled matrix instructions of CDNA4 take them as
+ * they are.
+ *   data    row r at data + r * row_stride; 16-byte aligned, row_stride a
+ *           multiple of 16 and at least the columns rounded up to 128.  The
+ *           bytes between the last column and that multiple of 128 must be zero
+ *           (reshard_block_quantize writes them so): products read them.
+ *   scales  block (R, C) at scales + R * scale_stride + C; any alignment,
+ *           scale_stride >= ceil(cols / 128).
+ * A plain matrix (F32, BF16, F16) is row-major with row_stride >= cols elements,
+ * at any address aligned to its element; block_rows is 0 and scales NULL.
+ *
+ * All calls here are asynchronous on `stream` (a hipStream_t of the current
+ * device; NULL = default stream), allocate nothing, hold no state between calls
+ * and may be captured into a HIP graph (each is one to three kernel launches).
+ * Pointers are borrowed as in reshard_execute; a matrix that is written must
+ * not overlap another one of the call.  Matrices with no elements are allowed
+ * (pointers and strides are not looked at).  Results do not depend on timing: no atomics, every sum
+ * in a fixed order.  Errors, checked before anything is launched:
+ * RESHARD_ERR_INVALID_ARGUMENT (shape, type, stride, alignment, overlap, host
+ * memory, workspace too small), RESHARD_ERR_NULL_SHARD (NULL data or scales of a
+ * matrix with elements), RESHARD_ERR_DEVICE_MISMATCH (a matrix or the stream on
+ * another device than the current one), RESHARD_ERR_HIP.
+ */
+#define RESHARD_BLOCK 128
+
+typedef struct reshard_matrix {
+  int64_t rows, cols;   /* at most 2^30 each */
+  int32_t dtype;        /* F32, BF16, F16 (plain) or FP8_E4M3, FP8_E5M2 (block-scaled) */
+  int32_t block_rows;   /* 0 (plain), 1 or 128 (block-scaled) */
+  void* data;
+  int64_t row_stride;   /* elements between rows */
+  void* scales;         /* one byte per block, NULL for a plain matrix */
+  int64_t scale_stride; /* bytes between rows of blocks */
+} reshard_matrix_t;
+
+/*
+ * Quantize the plain matrix src into the block-scaled dst of the same shape.
+ * With amax the largest finite magnitude of a block and top the format's largest
+ * value (448 for E4M3, 57344 for E5M2), the block's exponent is the smallest
+ * e >= -127 with amax <= top * 2^e (0 for a block without a finite value other
+ * than zero), its scale byte e + 127 and each element x / 2^e rounded to
+ * nearest, ties to even; infinities and NaN become NaN.  dst_t, NULL or a
+ * block-scaled matrix of the transposed shape, receives the same values
+ * transposed (for a product that contracts over the rows of src); it needs
+ * blocks of 128 rows on both sides.  Payload padding is written as zero; bytes
+ * beyond it, and rows beyond the matrices', are left as they were.
+ */
+reshard_status_t reshard_block_quantize(const reshard_matrix_t* src, const reshard_matrix_t* dst,
+                                        const reshard_matrix_t* dst_t, void* stream);
+
+/* Write the values a block-scaled matrix stands for into the plain matrix dst of
+ * the same shape, each rounded once (to nearest, ties to even; exact for F32, and
+ * for BF16 above its subnormal range). */
+reshard_status_t reshard_block_dequantize(const reshard_matrix_t* src, const reshard_matrix_t* dst, void* stream);
+
+/*
+ * out[m, n] = sum over k of a[m, k] * b[n, k]: the projection of activations a by
+ * a weight b stored output features first.  b is block-scaled; a is block-scaled,
+ * or plain, and then quantized to FP8_E4M3 in blocks of 1 x 128 within the call
+ * (the result is that of reshard_block_quantize followed by this call).  out is
+ * plain.  Sums are held in binary32 and rounded once to out's type.  For BF16 and
+ * F16 the products go through the 8-bit matrix instructions, which drop the low
+ * bits of small products beside large ones within one instruction (measured
+ * 1e-5 to 8e-5 of the result's norm, well under the output's rounding); for F32
+ * every product is exact.  An infinite element (E5M2) or a sum past binary32 gives an
+ * infinity or a NaN, as in floating point.
+ * workspace: device memory of at least reshard_block_matmul_workspace bytes (0:
+ * may be NULL), 16-byte aligned, not shared with a call that may run at the same
+ * time.  Its contents need no preparation.
+ */
+reshard_status_t reshard_block_matmul(const reshard_matrix_t* a, const reshard_matrix_t* b,
+                                      const reshard_matrix_t* out, void* workspace, int64_t workspace_bytes,
+                                      void* stream);
+
+/* Bytes of workspace reshard_block_matmul needs for matrices of these shapes and
+ * types (data and scales are not looked at and may be NULL).  Host only. */
+reshard_status_t reshard_block_matmul_workspace(const reshard_matrix_t* a, const reshard_matrix_t* b,
+                                                const reshard_matrix_t* out, int64_t* bytes);
+
+/*
+ * dw[n, k] = sum over m of dy[m, n] * x[m, k]: the weight gradient of that
+ * projection from the plain output gradient dy and the 8-bit checkpoint x of its
+ * input (block-scaled, blocks of 1 or 128 rows).  With `accumulate` nonzero
+ * the sum is added to what dw holds (in binary32, rounded once).  dy is used
+ * unrounded: an F16 or F32 value is cut into two or three bfloat16 parts
+ * that add up to it, each multiplied exactly; sums are held in binary32 (terms
+ * that stay below 2^-126, where the matrix instructions have no bits, may be
+ * lost).  An infinite dy or x gives an infinity or a NaN.  dw is plain.
+ * workspace: as for reshard_block_matmul, of reshard_block_grad_workspace bytes.
+ */
+reshard_status_t reshard_block_grad(const reshard_matrix_t* dy, const reshard_matrix_t* x,
+                                    const reshard_matrix_t* dw, int accumulate, void* workspace,
+                                    int64_t workspace_bytes, void* stream);
+reshard_status_t reshard_block_grad_workspace(const reshard_matrix_t* dy, const reshard_matrix_t* x,
+                                              const reshard_matrix_t* dw, int64_t* bytes);
+
 /* Message of the calling thread's last failed call ("" if none).  Valid until its next call. */
 const char* reshard_last_error(void);
 

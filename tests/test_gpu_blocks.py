@@ -1,0 +1,623 @@
+"""GPU tests of the block-scaled 8-bit operators against plain 64-bit forms
+(block_reference.py).
+
+Tolerances.  Quantizing and reading back are exact up to the one rounding the
+format defines, so they are compared bit for bit.  A product with F32 results
+multiplies exactly and adds K terms in binary32 in some order: each sum is off by
+at most K 2^-24 times the sum of the terms' magnitudes S (first order).  A 16-bit
+result adds half a step of its type, and the 8-bit matrix instruction may drop
+of each product what lies 18 bits below the largest product of its 128:
+at most 128 * 2^-18 = 2^-11 of S.
+"""
+import numpy as np
+import pytest
+import torch
+
+import block_reference as ref
+import dtensor_layout_movement_amd as R
+from block_reference import BLOCK, E4M3, E5M2
+from dtensor_layout_movement_amd import workloads as W
+from dtensor_layout_movement_amd.quantized import QuantizedPlan
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+CANARY = 0xA5
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a visible MI355X")
+    torch.cuda.set_device(0)
+    yield
+    torch.cuda.synchronize()
+
+
+def stream():
+    return torch.cuda.current_stream().cuda_stream
+
+
+class Plain:
+    """A plain matrix inside a larger buffer of canaries: any row stride and any
+    offset of its first element; rows behind the last and the bytes between
+    rows must stay as they were."""
+
+    def __init__(self, rows, cols, dtype, stride=None, offset=0, value=None):
+        self.rows, self.cols, self.dtype = rows, cols, dtype
+        self.stride = cols if stride is None else stride
+        size = torch.empty((), dtype=dtype).element_size()
+        n = offset + (rows + 2) * self.stride + 16
+        self.raw = torch.full((n * size,), CANARY, dtype=torch.uint8, device="cuda")
+        self.flat = self.raw.view(dtype)
+        self.offset = offset
+        self.view = self.flat[offset:offset + rows * self.stride].view(rows, self.stride)[:, :cols] \
+            if rows and self.stride else self.flat[:0].view(rows, cols)
+        if value is not None:
+            self.view.copy_(value)
+        self.m = R.matrix(rows, cols, R.dtype_code(dtype), self.flat.data_ptr() + offset * size, self.stride)
+        self.m.keep = self.raw  # the description borrows the memory
+
+    def check_rest(self):
+        """The bytes outside the matrix."""
+        size = self.raw.numel() // self.flat.numel()
+        keep = torch.ones(self.flat.numel(), dtype=torch.bool, device="cuda")
+        if self.rows and self.cols:
+            keep[self.offset:self.offset + self.rows * self.stride].view(self.rows, self.stride)[:, :self.cols] = False
+        assert bool((self.raw.view(-1, size)[keep] == CANARY).all())
+
+
+class Held:
+    """A block-scaled matrix with spare stride and canaries around."""
+
+    def __init__(self, rows, cols, block_rows, fmt=E4M3, extra=0, extra_scales=0):
+        self.rows, self.cols, self.block_rows, self.fmt = rows, cols, block_rows, fmt
+        self.width = -(-cols // BLOCK) * BLOCK
+        self.blocks = -(-cols // BLOCK)
+        self.srows = -(-rows // block_rows)
+        self.payload = torch.full((rows + 2, self.width + extra), CANARY, dtype=torch.uint8, device="cuda")
+        self.scales = torch.full((self.srows + 2, self.blocks + extra_scales), CANARY, dtype=torch.uint8, device="cuda")
+        self.m = R.matrix(rows, cols, fmt, self.payload.data_ptr(), self.payload.stride(0), block_rows,
+                          self.scales.data_ptr(), self.scales.stride(0))
+        self.m.keep = self.payload, self.scales
+
+    def check_rest(self):
+        assert bool((self.payload[:self.rows, self.cols:self.width] == 0).all())
+        assert bool((self.payload[:self.rows, self.width:] == CANARY).all())
+        assert bool((self.payload[self.rows:] == CANARY).all())
+        assert bool((self.scales[:self.srows, self.blocks:] == CANARY).all())
+        assert bool((self.scales[self.srows:] == CANARY).all())
+
+    def values(self):
+        return ref.values(self.payload, self.scales, self.rows, self.cols, self.block_rows, self.fmt)
+
+
+def values_of(shape, kind, seed, dtype):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(shape, generator=g)
+    if kind == "wide":  # magnitudes over the whole range, subnormals and zero blocks among them
+        x = x * torch.exp2(torch.randint(-140, 120, (shape[0], 1), generator=g).float())
+        x[:: 7] = 0
+    elif kind == "special":
+        x[torch.rand(shape, generator=g) < 0.02] = float("inf")
+        x[torch.rand(shape, generator=g) < 0.02] = -float("inf")
+        x[torch.rand(shape, generator=g) < 0.02] = float("nan")
+        x[torch.rand(shape, generator=g) < 0.02] = -0.0
+        if shape[0] > 2:
+            x[1] = float("nan")
+            x[2] = float("inf")
+    elif kind == "border":  # largest values at and around top * 2^e, ties between 8-bit values
+        x = torch.round(x * 64) / 64
+        x[:, 0] = 448.0 * torch.exp2(torch.randint(-4, 4, (shape[0],), generator=g).float())
+        x[1::2, 0] = torch.nextafter(x[1::2, 0], torch.tensor(float("inf")))
+    return x.to(dtype)
+
+
+def quantized(x, block_rows, fmt=E4M3, **kw):
+    h = Held(x.shape[0], x.shape[1], block_rows, fmt, **kw)
+    p = Plain(x.shape[0], x.shape[1], x.dtype, value=x)
+    R.reshard_block_quantize(p.m, h.m, None, stream())
+    return h
+
+
+SHAPES = [(1, 1), (1, 128), (3, 127), (5, 129), (128, 128), (129, 16), (130, 300), (257, 515), (300, 1025)]
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("fmt", [E4M3, E5M2])
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_quantize_matches_the_definition(shape, block_rows, fmt, dtype):
+    rows, cols = shape
+    for i, kind in enumerate(("normal", "wide", "special", "border")):
+        x = values_of(shape, kind, 10 * rows + i, DTYPES[dtype])
+        src = Plain(rows, cols, DTYPES[dtype], stride=cols + (3 if i % 2 else 0), offset=i, value=x)
+        dst = Held(rows, cols, block_rows, fmt, extra=16 * (i % 2), extra_scales=i)
+        R.reshard_block_quantize(src.m, dst.m, None, stream())
+        torch.cuda.synchronize()
+        want, scales = ref.quantize(x, block_rows, fmt)
+        assert np.array_equal(dst.scales[:dst.srows, :dst.blocks].cpu().numpy(), scales), kind
+        got = dst.values()
+        assert np.array_equal(got, want, equal_nan=True), kind
+        assert np.array_equal(np.signbit(got)[~np.isnan(got)], np.signbit(want)[~np.isnan(want)]), kind
+        dst.check_rest()
+        src.check_rest()
+
+
+@pytest.mark.parametrize("fmt", [E4M3, E5M2])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_quantize_with_transpose(shape, fmt):
+    rows, cols = shape
+    x = values_of(shape, "special", 3, torch.float32)
+    src = Plain(rows, cols, torch.float32, value=x)
+    dst, dst_t = Held(rows, cols, 128, fmt, extra=32), Held(cols, rows, 128, fmt, extra_scales=2)
+    R.reshard_block_quantize(src.m, dst.m, dst_t.m, stream())
+    torch.cuda.synchronize()
+    want, scales = ref.quantize(x, 128, fmt)
+    assert np.array_equal(dst.values(), want, equal_nan=True)
+    assert np.array_equal(dst_t.values(), want.T, equal_nan=True)
+    assert np.array_equal(dst_t.scales[:dst_t.srows, :dst_t.blocks].cpu().numpy(), scales.T)
+    dst.check_rest()
+    dst_t.check_rest()
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("fmt", [E4M3, E5M2])
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_dequantize_rounds_each_value_once(shape, block_rows, fmt, dtype):
+    """Every byte under every scale that fits, the scale 255 (NaN) among them."""
+    rows, cols = shape
+    g = torch.Generator().manual_seed(rows + cols)
+    h = Held(rows, cols, block_rows, fmt, extra=48, extra_scales=1)
+    h.payload[:rows, :h.width] = torch.randint(0, 256, (rows, h.width), generator=g).to(torch.uint8).cuda()
+    h.scales[:h.srows, :h.blocks] = torch.randint(0, 256, (h.srows, h.blocks), generator=g).to(torch.uint8).cuda()
+    out = Plain(rows, cols, DTYPES[dtype], stride=cols + 5, offset=3)
+    R.reshard_block_dequantize(h.m, out.m, stream())
+    torch.cuda.synchronize()
+    with np.errstate(over="ignore"):
+        # q 2^e has at most four significant bits: binary32 holds it exactly, or it is
+        # infinite, and the cast from there is the one rounding
+        want = torch.from_numpy(h.values().astype(np.float32)).to(DTYPES[dtype])
+    got = out.view.cpu()
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(got[~torch.isnan(got)], want[~torch.isnan(want)])
+    out.check_rest()
+
+
+# ------------------------------------------------------------------ products
+
+
+def workspace(n):
+    t = torch.full((n + 64,), CANARY, dtype=torch.uint8, device="cuda")
+    return t, (t.data_ptr(), n)
+
+
+def check_product(got, want, mass, terms, dtype, eight_bit):
+    """got against the float64 sum `want` of `terms` terms whose magnitudes add
+    up to `mass`."""
+    got = got.double().cpu().numpy()
+    tol = terms * 2.0 ** -24 * mass
+    if eight_bit and dtype != torch.float32:
+        tol = tol + 2.0 ** -11 * mass
+    if dtype != torch.float32:
+        tol = tol * (1 + ref.rounding(dtype)) + ref.rounding(dtype) * np.abs(want) + torch.finfo(dtype).tiny * ref.rounding(dtype)
+    else:
+        tol = tol + ref.rounding(dtype) * np.abs(want)
+    bad = ~(np.abs(got - want) <= tol)
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:3], got[bad][:3], want[bad][:3], tol[bad][:3])
+
+
+def matmul(a_m, b_m, out):
+    need = R.reshard_block_matmul_workspace(a_m, b_m, out.m)
+    room, args = workspace(need)
+    R.reshard_block_matmul(a_m, b_m, out.m, *args, stream())
+    torch.cuda.synchronize()
+    assert bool((room[need:] == CANARY).all())
+    out.check_rest()
+
+
+MATMULS = [(1, 1, 1), (1, 16, 128), (1, 300, 4096), (2, 130, 200), (16, 128, 512), (17, 129, 129), (33, 257, 1000),
+           (64, 64, 64), (65, 640, 256), (128, 256, 640), (130, 250, 385), (257, 513, 300), (300, 1025, 131), (512, 512, 1024)]
+
+
+@pytest.mark.parametrize("out_type", list(DTYPES))
+@pytest.mark.parametrize("formats", [(E4M3, E4M3), (E5M2, E4M3), (E4M3, E5M2), (E5M2, E5M2)], ids=str)
+@pytest.mark.parametrize("mnk", MATMULS, ids=str)
+def test_matmul_of_held_operands(mnk, formats, out_type):
+    m, n, k = mnk
+    dtype = DTYPES[out_type]
+    for block_a, block_b in ((1, 128), (128, 1)):
+        a = quantized(values_of((m, k), "normal", m + n, torch.float32), block_a, formats[0], extra=16)
+        b = quantized(values_of((n, k), "normal", n + k, torch.float32), block_b, formats[1], extra_scales=3)
+        out = Plain(m, n, dtype, stride=n + 7, offset=1)
+        matmul(a.m, b.m, out)
+        av, bv = a.values(), b.values()
+        check_product(out.view, av @ bv.T, np.abs(av) @ np.abs(bv).T, k, dtype, True)
+
+
+@pytest.mark.parametrize("in_type", list(DTYPES))
+@pytest.mark.parametrize("mnk", MATMULS, ids=str)
+def test_matmul_quantizes_a_plain_operand(mnk, in_type):
+    """The same bytes out as with a quantized first, whatever the input's stride."""
+    m, n, k = mnk
+    dtype = DTYPES[in_type]
+    x = values_of((m, k), "normal", 3 * m + k, dtype)
+    b = quantized(values_of((n, k), "normal", n + k, torch.float32), 128)
+    for stride, offset in ((k, 0), (k + 3, 1)):
+        a = Plain(m, k, dtype, stride=stride, offset=offset, value=x)
+        out, two = Plain(m, n, dtype), Plain(m, n, dtype)
+        matmul(a.m, b.m, out)
+        q = quantized(x, 1)
+        av, bv = q.values(), b.values()
+        check_product(out.view, av @ bv.T, np.abs(av) @ np.abs(bv).T, k, dtype, True)
+        matmul(q.m, b.m, two)
+        check_product(two.view, av @ bv.T, np.abs(av) @ np.abs(bv).T, k, dtype, True)
+
+
+def test_matmul_scales_over_the_whole_range():
+    """Blocks whose scales are far apart within one row of the result."""
+    m, n, k = 40, 70, 512
+    a = values_of((m, k), "normal", 1, torch.float32)
+    b = values_of((n, k), "normal", 2, torch.float32)
+    for j in range(4):
+        a[:, j * 128:(j + 1) * 128] *= 2.0 ** (40 * (j - 2))
+        b[:, j * 128:(j + 1) * 128] *= 2.0 ** (-40 * (j - 2) + 7 * j)
+    for dtype in (torch.float32, torch.bfloat16):
+        qa, qb = quantized(a, 1), quantized(b, 128)
+        out = Plain(m, n, dtype)
+        matmul(qa.m, qb.m, out)
+        av, bv = qa.values(), qb.values()
+        check_product(out.view, av @ bv.T, np.abs(av) @ np.abs(bv).T, k, dtype, True)
+
+
+@pytest.mark.parametrize("out_type", ["f32", "bf16"])
+@pytest.mark.parametrize("m", [3, 70, 300])
+def test_matmul_not_a_number_stays_in_its_row_and_column(m, out_type):
+    n, k = 140, 260
+    a, b = values_of((m, k), "normal", 5, torch.float32), values_of((n, k), "normal", 6, torch.float32)
+    a[1, 7], a[2, 200], b[133, 259] = float("nan"), float("inf"), -float("inf")
+    qa, qb = quantized(a, 1), quantized(b, 128)
+    out = Plain(m, n, DTYPES[out_type])
+    matmul(qa.m, qb.m, out)
+    nan = torch.isnan(out.view.float()).cpu()
+    want = torch.zeros(m, n, dtype=torch.bool)
+    want[1], want[2], want[:, 133] = True, True, True
+    assert torch.equal(nan, want)
+
+
+@pytest.mark.parametrize("mnk", [(0, 5, 130), (5, 0, 130), (5, 7, 0), (0, 0, 0), (70, 3, 0), (300, 300, 0)], ids=str)
+def test_matmul_with_empty_sides(mnk):
+    m, n, k = mnk
+    a = Plain(m, k, torch.bfloat16, value=torch.ones(m, k)).m
+    b = Held(n, k, 128)
+    b.payload.zero_(), b.scales.fill_(127)
+    out = Plain(m, n, torch.bfloat16)
+    matmul(a, b.m, out)
+    assert bool((out.view == 0).all())  # an empty sum; or nothing to write
+
+
+# ------------------------------------------------------------------ gradients
+
+
+def grad(dy, x_m, dw, accumulate=False):
+    need = R.reshard_block_grad_workspace(dy.m, x_m, dw.m)
+    room, args = workspace(need)
+    R.reshard_block_grad(dy.m, x_m, dw.m, accumulate, *args, stream())
+    torch.cuda.synchronize()
+    assert bool((room[need:] == CANARY).all())
+    dw.check_rest()
+
+
+GRADS = [(1, 1, 1), (1, 128, 130), (2, 17, 300), (31, 64, 64), (32, 65, 129), (33, 130, 128), (64, 256, 256),
+         (100, 300, 515), (257, 129, 385), (1000, 100, 130), (4096, 64, 128), (515, 640, 768)]
+
+
+@pytest.mark.parametrize("dy_type,dw_type", [("bf16", "bf16"), ("bf16", "f32"), ("f16", "f32"), ("f16", "f16"),
+                                             ("f32", "f32"), ("f32", "bf16")])
+@pytest.mark.parametrize("mnk", GRADS, ids=str)
+def test_grad_of_the_weight(mnk, dy_type, dw_type):
+    m, n, k = mnk
+    for block_rows, fmt, stride, offset in ((1, E4M3, n, 0), (128, E5M2, n + 5, 3), (1, E4M3, -(-n // 8) * 8, 8)):
+        g = values_of((m, n), "normal", m + k, torch.float32).to(DTYPES[dy_type])
+        dy = Plain(m, n, DTYPES[dy_type], stride=stride, offset=offset, value=g)
+        x = quantized(values_of((m, k), "normal", m + n, torch.float32), block_rows, fmt, extra=16, extra_scales=1)
+        dw = Plain(n, k, DTYPES[dw_type], stride=k + 3, offset=1)
+        grad(dy, x.m, dw)
+        gv, xv = g.double().numpy(), x.values()
+        want, mass = gv.T @ xv, np.abs(gv).T @ np.abs(xv)
+        # an fp16 or fp32 term goes in as two or three
+        terms = m * {"bf16": 1, "f16": 2, "f32": 3}[dy_type]
+        check_product(dw.view, want, mass, terms, DTYPES[dw_type], False)
+
+
+@pytest.mark.parametrize("dw_type", list(DTYPES))
+@pytest.mark.parametrize("mnk", [(40, 70, 200), (700, 130, 130), (0, 40, 200)], ids=str)
+def test_grad_accumulates(mnk, dw_type):
+    m, n, k = mnk
+    dtype = DTYPES[dw_type]
+    before = values_of((n, k), "normal", 9, dtype)
+    g = values_of((m, n), "normal", 7, torch.bfloat16)
+    dy = Plain(m, n, torch.bfloat16, value=g)
+    x = quantized(values_of((m, k), "normal", 8, torch.float32), 1) if m else Held(0, k, 1)
+    dw = Plain(n, k, dtype, value=before)
+    grad(dy, x.m, dw, accumulate=True)
+    gv, xv = g.double().numpy(), x.values() if m else np.zeros((0, k))
+    old = before.double().numpy()
+    check_product(dw.view, gv.T @ xv + old, np.abs(gv).T @ np.abs(xv) + np.abs(old), m + 1, dtype, False)
+    if not m:
+        assert torch.equal(dw.view.cpu(), before)
+
+
+def test_grad_of_empty_sides_and_zero_rows():
+    dw = Plain(40, 200, torch.float32)
+    grad(Plain(0, 40, torch.bfloat16), Held(0, 200, 1).m, dw)
+    assert bool((dw.view == 0).all())
+    grad(Plain(5, 0, torch.bfloat16), quantized(values_of((5, 200), "normal", 1, torch.float32), 1).m,
+         Plain(0, 200, torch.float32))
+
+
+@pytest.mark.parametrize("dy_type", list(DTYPES))
+def test_grad_not_a_number_stays_in_its_row_and_column(dy_type):
+    m, n, k = 90, 70, 300
+    g = values_of((m, n), "normal", 1, DTYPES[dy_type])
+    x = values_of((m, k), "normal", 2, torch.float32)
+    g[3, 11], g[50, 20], x[80, 299] = float("nan"), float("inf"), float("nan")
+    dw = Plain(n, k, torch.float32)
+    grad(Plain(m, n, DTYPES[dy_type], value=g), quantized(x, 1).m, dw)
+    bad = ~torch.isfinite(dw.view).cpu()
+    want = torch.zeros(n, k, dtype=torch.bool)
+    want[11], want[20], want[:, 299] = True, True, True
+    assert torch.equal(bad, want)
+    assert bool(torch.isnan(dw.view[11]).all())
+
+
+def test_grad_f32_keeps_every_bit_of_dy():
+    """One row and x = 1: the gradient is dy itself, bit for bit."""
+    n, k = 200, 128
+    g = values_of((1, n), "normal", 4, torch.float32)
+    g[0, :3] = torch.tensor([1 + 2.0 ** -23, -3.4028234e38, 1.17549435e-38 * 2.0 ** 20])
+    dw = Plain(n, k, torch.float32)
+    grad(Plain(1, n, torch.float32, value=g), quantized(torch.ones(1, k), 1).m, dw)
+    assert torch.equal(dw.view.cpu(), g[0][:, None].expand(n, k))
+
+
+def test_gradients_against_differences():
+    """A projection's gradients from the operators against central differences of
+    the projection itself, in float64 over the values that the 8-bit operands
+    stand for: loss = sum of (x^ w^T) * c is linear in w^ and in x^, so that the
+    difference quotient is exact up to float64 rounding."""
+    m, n, k = 37, 40, 150
+    x = quantized(values_of((m, k), "normal", 1, torch.float32), 1)
+    w_src = Plain(n, k, torch.float32, value=values_of((n, k), "normal", 2, torch.float32))
+    w, wt = Held(n, k, 128), Held(k, n, 128)
+    R.reshard_block_quantize(w_src.m, w.m, wt.m, stream())
+    c = quantized(values_of((m, n), "normal", 3, torch.float32), 1)  # dy whose 8-bit form is itself
+    dy = Plain(m, n, torch.float32)
+    R.reshard_block_dequantize(c.m, dy.m, stream())
+    dx, dw = Plain(m, k, torch.float32), Plain(n, k, torch.float32)
+    matmul(dy.m, wt.m, dx)
+    grad(dy, x.m, dw)
+    xv, wv, cv = x.values(), w.values(), dy.view.double().cpu().numpy()
+    loss = lambda xx, ww: float(((xx @ ww.T) * cv).sum())
+    rng = np.random.default_rng(0)
+    h = 2.0 ** -6
+    for _ in range(40):
+        i, j, r = rng.integers(n), rng.integers(k), rng.integers(m)
+        up, down = wv.copy(), wv.copy()
+        up[i, j] += h
+        down[i, j] -= h
+        d = (loss(xv, up) - loss(xv, down)) / (2 * h)
+        assert abs(dw.view[i, j].item() - d) <= 1e-9 + 3 * m * 2.0 ** -24 * (np.abs(cv[:, i]) @ np.abs(xv[:, j]))
+        up, down = xv.copy(), xv.copy()
+        up[r, j] += h
+        down[r, j] -= h
+        d = (loss(up, wv) - loss(down, wv)) / (2 * h)
+        assert abs(dx.view[r, j].item() - d) <= 1e-9 + n * 2.0 ** -24 * (np.abs(cv[r]) @ np.abs(wv[:, j]))
+
+
+# ------------------------------------------------- streams, graphs, refusals
+
+
+def test_host_memory_is_refused():
+    x = torch.ones(4, 128, dtype=torch.bfloat16)
+    h = Held(4, 128, 1)
+    with pytest.raises(R.ReshardError) as e:
+        R.reshard_block_quantize(R.matrix(4, 128, R.DTYPE_BF16, x.data_ptr()), h.m, None, stream())
+    assert e.value.status == R.ERR_INVALID_ARGUMENT and "src" in str(e.value)
+    torch.cuda.synchronize()
+    assert bool((h.payload == CANARY).all())
+
+
+def test_another_stream_and_two_calls_at_once():
+    """Two products on two streams with workspaces of their own."""
+    m, n, k = 200, 300, 515
+    cases = []
+    for s in range(2):
+        x = values_of((m, k), "normal", s, torch.bfloat16)
+        b = quantized(values_of((n, k), "normal", 10 + s, torch.float32), 128)
+        a, out = Plain(m, k, torch.bfloat16, value=x), Plain(m, n, torch.bfloat16)
+        room, args = workspace(R.reshard_block_matmul_workspace(a.m, b.m, out.m))
+        cases.append((a, b, out, room, args, torch.cuda.Stream(), x))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for a, b, out, room, args, st, x in cases:
+            R.reshard_block_matmul(a.m, b.m, out.m, *args, st.cuda_stream)
+    torch.cuda.synchronize()
+    for a, b, out, room, args, st, x in cases:
+        av, bv = quantized(x, 1).values(), b.values()
+        check_product(out.view, av @ bv.T, np.abs(av) @ np.abs(bv).T, k, torch.bfloat16, True)
+
+
+@pytest.mark.parametrize("m", [1, 40, 300])
+def test_a_training_step_captured_and_replayed(m):
+    """Quantize, project, input and weight gradients in one graph, replayed with
+    new inputs and eager work in between: equal to the eager calls bit for bit."""
+    n, k = 260, 390
+    w_src = Plain(n, k, torch.float32, value=values_of((n, k), "normal", 1, torch.float32))
+    xs, dys = Plain(m, k, torch.bfloat16), Plain(m, n, torch.bfloat16)
+    w, wt, x = Held(n, k, 128), Held(k, n, 128), Held(m, k, 1)
+    outs = [Plain(m, n, torch.bfloat16), Plain(m, k, torch.bfloat16), Plain(n, k, torch.float32)]
+    need = max(R.reshard_block_matmul_workspace(x.m, w.m, outs[0].m),
+               R.reshard_block_matmul_workspace(dys.m, wt.m, outs[1].m),
+               R.reshard_block_grad_workspace(dys.m, x.m, outs[2].m))
+    room, args = workspace(need)
+
+    def step():
+        R.reshard_block_quantize(w_src.m, w.m, wt.m, stream())
+        R.reshard_block_quantize(xs.m, x.m, None, stream())
+        R.reshard_block_matmul(x.m, w.m, outs[0].m, *args, stream())
+        R.reshard_block_matmul(dys.m, wt.m, outs[1].m, *args, stream())
+        R.reshard_block_grad(dys.m, x.m, outs[2].m, False, *args, stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for seed in range(4):
+        xs.view.copy_(values_of((m, k), "normal", 20 + seed, torch.bfloat16))
+        dys.view.copy_(values_of((m, n), "normal", 30 + seed, torch.bfloat16))
+        step()
+        torch.cuda.synchronize()
+        eager = [o.view.clone() for o in outs]
+        for o in outs:
+            o.view.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        for o, e in zip(outs, eager):
+            assert torch.equal(o.view, e)
+            o.check_rest()
+
+
+def test_offsets_past_32_bits():
+    """A payload whose last rows lie beyond 4 GiB."""
+    rows, cols = 70000, 128
+    stride = 65536
+    payload = torch.empty(rows * stride, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(rows, 1, dtype=torch.uint8, device="cuda")
+    x = values_of((rows, cols), "normal", 1, torch.bfloat16)
+    src = Plain(rows, cols, torch.bfloat16, value=x)
+    h = R.matrix(rows, cols, E4M3, payload.data_ptr(), stride, 1, scales.data_ptr(), 1)
+    back = Plain(rows, cols, torch.bfloat16)
+    R.reshard_block_quantize(src.m, h, None, stream())
+    R.reshard_block_dequantize(h, back.m, stream())
+    w = quantized(values_of((32, cols), "normal", 2, torch.float32), 128)
+    out, dw = Plain(rows, 32, torch.float32), Plain(32, cols, torch.float32)
+    matmul(h, w.m, out)
+    dy = Plain(rows, 32, torch.bfloat16, value=values_of((rows, 32), "normal", 3, torch.bfloat16))
+    grad(dy, h, dw)
+    tail = slice(rows - 300, rows)
+    want, _ = ref.quantize(x[tail], 1)
+    assert np.array_equal(back.view[tail].double().cpu().numpy(), want)
+    wv = w.values()
+    check_product(out.view[tail], want @ wv.T, np.abs(want) @ np.abs(wv).T, cols, torch.float32, True)
+    xv, gv = back.view.double().cpu().numpy(), dy.view.double().cpu().numpy()
+    check_product(dw.view, gv.T @ xv, np.abs(gv).T @ np.abs(xv), rows, torch.float32, False)
+    src.check_rest()
+
+
+def test_results_do_not_change_from_call_to_call():
+    m, n, k = 130, 515, 2000
+    a = quantized(values_of((m, k), "normal", 1, torch.float32), 1)
+    b = quantized(values_of((n, k), "normal", 2, torch.float32), 128)
+    dy = Plain(m, n, torch.float32, value=values_of((m, n), "normal", 3, torch.float32))
+    first = None
+    for _ in range(5):
+        out, dw = Plain(m, n, torch.float32), Plain(n, k, torch.float32)
+        matmul(a.m, b.m, out)
+        grad(dy, a.m, dw)
+        if first is None:
+            first = out.view.clone(), dw.view.clone()
+        assert torch.equal(out.view, first[0]) and torch.equal(dw.view, first[1])
+
+
+# ------------------------------------------------------------ the whole run
+
+
+def byte_buffers(shapes):
+    return [torch.full((max(1, r * c),), CANARY, dtype=torch.uint8, device="cuda") for r, c in shapes]
+
+
+def test_refit_to_8_bits_then_project_and_train():
+    """An up- and a down-projection held by two trainer ranks are refitted to
+    8 bits on 2 x 2 inference ranks.  Each inference rank's shard equals that
+    part of the quantized whole.  The up-projection splits its output columns
+    over ranks; the down-projection's per-rank products are Partial sums that a
+    plain reshard adds up.  The trainer's weight gradient from the 8-bit
+    checkpoint is held by two data-parallel ranks and added the same way."""
+    hidden, ffn, tokens = 256, 1024, 70
+    T = W.TensorSpec
+    specs = [T("up", (ffn, hidden), torch.float32, (2,), (0,), (2, 2), (W.R, 0)),
+             T("down", (hidden, ffn), torch.float32, (2,), (1,), (2, 2), (W.R, 1))]
+    whole = [values_of(s.shape, "normal", 40 + t, torch.float32) for t, s in enumerate(specs)]
+    shards = [[p.contiguous().cuda() for p in whole[0].chunk(2, 0)], [p.contiguous().cuda() for p in whole[1].chunk(2, 1)]]
+    plan = QuantizedPlan(specs)
+    try:
+        bufs = {(side, what): [byte_buffers(getattr(plan, what + "_shapes")(t, side)) for t in range(2)]
+                for side in ("src", "dst") for what in ("payload", "scale")}
+        ptrs = {k: [[b.data_ptr() for b in per] for per in v] for k, v in bufs.items()}
+        bound = plan.bind([[s.data_ptr() for s in per] for per in shards], ptrs["src", "payload"], ptrs["src", "scale"],
+                          ptrs["dst", "payload"], ptrs["dst", "scale"])
+        R.reshard_plan_upload(plan.plan, stream())
+        for _ in range(2):
+            plan.execute(bound, stream())
+        torch.cuda.synchronize()
+        want = [ref.quantize(w, 128)[0] for w in whole]
+        weights = []
+        for t in range(2):
+            per = []
+            for rank in range(4):
+                half = np.split(want[t], 2, axis=t)[rank % 2]  # up: rows, down: columns
+                q = bufs["dst", "payload"][t][rank].view(plan.payload_shapes(t, "dst")[rank])
+                s = bufs["dst", "scale"][t][rank].view(plan.scale_shapes(t, "dst")[rank])
+                assert np.array_equal(ref.values(q, s, *half.shape, 128), half), (t, rank)
+                per.append(plan.weight(t, rank, ptrs["dst", "payload"][t][rank], ptrs["dst", "scale"][t][rank]))
+            weights.append(per)
+        x = values_of((tokens, hidden), "normal", 1, torch.bfloat16)
+        xin = Plain(tokens, hidden, torch.bfloat16, value=x)
+        xq, _ = ref.quantize(x, 1)
+        hidden_act = Plain(tokens, ffn, torch.bfloat16)
+        for rank in range(2):  # each writes its half of the columns
+            half = R.matrix(tokens, ffn // 2, R.DTYPE_BF16, hidden_act.view.data_ptr() + rank * ffn, ffn)
+            need = R.reshard_block_matmul_workspace(xin.m, weights[0][rank], half)
+            room, args = workspace(need)
+            R.reshard_block_matmul(xin.m, weights[0][rank], half, *args, stream())
+        torch.cuda.synchronize()
+        check_product(hidden_act.view, xq @ want[0].T, np.abs(xq) @ np.abs(want[0]).T, hidden, torch.bfloat16, True)
+        hq, _ = ref.quantize(hidden_act.view, 1)
+        parts = [Plain(tokens, hidden, torch.float32) for _ in range(2)]
+        for rank in range(2):
+            half = R.matrix(tokens, ffn // 2, R.DTYPE_BF16, hidden_act.view.data_ptr() + rank * ffn, ffn)
+            need = R.reshard_block_matmul_workspace(half, weights[1][rank], parts[rank].m)
+            room, args = workspace(need)
+            R.reshard_block_matmul(half, weights[1][rank], parts[rank].m, *args, stream())
+        total = torch.empty(tokens, hidden, device="cuda")
+        add_partial([p.view for p in parts], total)
+        check_product(total, hq @ want[1].T, np.abs(hq) @ np.abs(want[1]).T, ffn + 2, torch.float32, True)
+        # the trainer: dw of the up-projection, tokens split over two data-parallel ranks
+        dy = values_of((tokens, ffn), "normal", 2, torch.bfloat16)
+        grads = []
+        for rows in (slice(0, 35), slice(35, tokens)):
+            ckpt = quantized(x[rows], 1)
+            g = Plain(35, ffn, torch.bfloat16, value=dy[rows])
+            dw = Plain(ffn, hidden, torch.float32)
+            grad(g, ckpt.m, dw)
+            grads.append(dw.view)
+        total = torch.empty(ffn, hidden, device="cuda")
+        add_partial(grads, total)
+        gv = dy.double().numpy()
+        check_product(total, gv.T @ xq, np.abs(gv).T @ np.abs(xq), tokens + 2, torch.float32, False)
+    finally:
+        plan.close()
+
+
+def add_partial(parts, out):
+    """Sum of contiguous per-rank contributions by a Partial -> Replicate reshard."""
+    shape = tuple(out.shape)
+    src = R.reshard_layout_create(shape, R.DTYPE_F32, (len(parts),), (R.PARTIAL,))
+    dst = R.reshard_layout_create(shape, R.DTYPE_F32, (1,), (R.REPLICATE,))
+    plan = R.reshard_plan_create(src, dst)
+    parts = [p.contiguous() for p in parts]
+    R.reshard_execute(plan, [p.data_ptr() for p in parts], [out.data_ptr()], stream())
+    torch.cuda.synchronize()
+    R.reshard_plan_destroy(plan)
+    R.reshard_layout_destroy(src)
+    R.reshard_layout_destroy(dst)
