@@ -31,6 +31,7 @@ hipError_t launch_dequantize(const reshard_matrix_t& src, const reshard_matrix_t
 
 // How a product runs: workspace bytes and launches.
 struct MatmulPlan {
+  int tile = 0;              // rows and columns of a tile (0: the form for few rows)
   int64_t groups = 0;        // workgroups of the product
   int64_t quantized = 0;     // bytes of a's quantized payload in the workspace (0: not needed)
   int64_t quantized_scales = 0;

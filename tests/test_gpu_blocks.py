@@ -255,6 +255,22 @@ def test_matmul_quantizes_a_plain_operand(mnk, in_type):
         check_product(two.view, av @ bv.T, np.abs(av) @ np.abs(bv).T, k, dtype, True)
 
 
+@pytest.mark.parametrize("mnk", [(300, 24600, 300), (2100, 6000, 131), (6400, 2049, 1153), (513, 25000, 640)], ids=str)
+@pytest.mark.parametrize("formats", [(E4M3, E4M3), (E5M2, E5M2)], ids=str)
+def test_matmul_of_many_tiles(mnk, formats):
+    """Enough rows and columns for the largest tiles, one, odd and even numbers
+    of steps; the 64-bit product on the GPU."""
+    m, n, k = mnk
+    a = quantized(values_of((m, k), "normal", m, torch.float32), 1, formats[0], extra=16)
+    b = quantized(values_of((n, k), "normal", n, torch.float32), 128, formats[1], extra_scales=3)
+    out = Plain(m, n, torch.bfloat16, stride=n + 1, offset=1)
+    matmul(a.m, b.m, out)
+    av, bv = torch.from_numpy(a.values()).cuda(), torch.from_numpy(b.values()).cuda()
+    want, mass = av @ bv.t(), av.abs() @ bv.abs().t()
+    tol = (k * 2.0 ** -24 + 2.0 ** -11) * mass * (1 + ref.rounding(torch.bfloat16)) + ref.rounding(torch.bfloat16) * want.abs()
+    assert bool(((out.view.double() - want).abs() <= tol + 1e-38).all())
+
+
 def test_matmul_scales_over_the_whole_range():
     """Blocks whose scales are far apart within one row of the result."""
     m, n, k = 40, 70, 512
