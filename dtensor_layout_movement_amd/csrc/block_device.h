@@ -17,6 +17,27 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
+// Keeps a value in registers at this point of the program: no use of it moves
+// above, no computation of it below.
+template <typename T> __device__ __forceinline__ void pin(T& x) {
+#ifdef __HIP_DEVICE_COMPILE__
+  asm volatile("" : "+v"(x));
+#endif
+}
+
+// Memory read by 32-bit offsets (no load reaches past its `bytes`).
+typedef __amdgpu_buffer_rsrc_t Buffer;
+__device__ __forceinline__ Buffer buffer_of(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, int(bytes), 0x00020000);
+}
+
+// 16 bytes a lane from `lane_off + off` straight to LDS: lane l's to byte 16 l from
+// `to` on, the same `to` and `off` for the whole wave.
+__device__ __forceinline__ void load_to_lds(Buffer from, uint8_t* to, uint32_t lane_off, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) uint32_t*)to, 16, int(lane_off),
+                                           int(off), 0, 0);
+}
+
 // Element types by their dtype code.
 template <int DT> struct Elem;
 template <> struct Elem<RESHARD_DTYPE_F32> {

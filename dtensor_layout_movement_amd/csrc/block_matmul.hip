@@ -113,21 +113,17 @@ __device__ __forceinline__ int slot_of(int row, int chunk) { return chunk ^ ((ro
 
 // Moves a tile's rows, 128 bytes from column byte `col` of each, into `to`.
 template <int ROWS, int THREADS>
-__device__ __forceinline__ void stage(__amdgpu_buffer_rsrc_t base, const uint32_t (&off)[ROWS * 8 / THREADS],
+__device__ __forceinline__ void stage(Buffer base, const uint32_t (&off)[ROWS * 8 / THREADS],
                                       uint32_t col, uint8_t* to, int wave) {
 #pragma unroll
-  for (int i = 0; i < ROWS * 8 / THREADS; ++i)
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        base, (__attribute__((address_space(3))) uint32_t*)(to + (i * THREADS + wave * 64) * 16), 16, int(off[i]),
-        int(col), 0, 0);
+  for (int i = 0; i < ROWS * 8 / THREADS; ++i) load_to_lds(base, to + (i * THREADS + wave * 64) * 16, off[i], col);
 }
 
 // The operand's rows from r0 on as a buffer: 32-bit offsets for its loads, and
 // none past its end.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const Operand& o, int r0, int rows, uint32_t blocks) {
+__device__ __forceinline__ Buffer rows_of(const Operand& o, int r0, int rows, uint32_t blocks) {
   const int last = min(r0 + rows, o.rows) - 1 - r0;
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(o.data + r0 * o.stride), 0,
-                                           int(uint32_t(last) * uint32_t(o.stride) + blocks * kBlock), 0x00020000);
+  return buffer_of(o.data + r0 * o.stride, uint32_t(last) * uint32_t(o.stride) + blocks * kBlock);
 }
 
 // A lane's offsets (row and chunk) in the staging of the rows from r0 on; rows
@@ -176,7 +172,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tiles(Operand a, Opera
   uint32_t off_a[BM * 8 / kThreads], off_b[BN * 8 / kThreads];
   stage_offsets<BM, kThreads>(a, m0, off_a);
   stage_offsets<BN, kThreads>(b, n0, off_b);
-  const __amdgpu_buffer_rsrc_t base_a = buffer_of(a, m0, BM, blocks), base_b = buffer_of(b, n0, BN, blocks);
+  const Buffer base_a = rows_of(a, m0, BM, blocks), base_b = rows_of(b, n0, BN, blocks);
   const auto load = [&](uint8_t* to, uint32_t k) {
     stage<BM, kThreads>(base_a, off_a, k * kBlock, to, wave);
     stage<BN, kThreads>(base_b, off_b, k * kBlock, to + BM * kBlock, wave);
@@ -242,7 +238,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tiles(Operand a, Opera
 #pragma unroll
       for (int i = 0; i < kN; ++i) {
         acc[i][j] = step128<kExact, E5_B, E5_A>(y[i], sb[i], x, sa, acc[i][j]);
-        asm volatile("" : "+v"(acc[i][j]));
+        pin(acc[i][j]);
       }
       __builtin_amdgcn_sched_barrier(0);
       x = next;

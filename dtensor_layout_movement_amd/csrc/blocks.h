@@ -41,9 +41,25 @@ MatmulPlan plan_matmul(const reshard_matrix_t& a, const reshard_matrix_t& b, con
 hipError_t launch_matmul(const MatmulPlan& plan, const reshard_matrix_t& a, const reshard_matrix_t& b,
                          const reshard_matrix_t& out, void* workspace, hipStream_t stream);
 
+// Sums n_parts binary32 matrices (rows of out.cols rounded up to 4 elements,
+// `part_stride` elements apart) in order into `out`, or adds the sum to it.
+hipError_t launch_join(const float* parts, int n_parts, int64_t part_stride, const reshard_matrix_t& out,
+                       bool accumulate, hipStream_t stream);
+
+// Columns of dy and rows of dy times its bfloat16 planes, at most: a step's rows
+// within 32-bit offsets, and rows in 32 bits.
+constexpr int64_t kMaxGradCols = int64_t(1) << 24, kMaxGradRows = int64_t(3) << 29;
+int64_t grad_planes(int dtype);
+
 struct GradPlan {
+  int tile = 0;                  // rows and columns of a tile of dw
+  int splits = 1;                // workgroups that share a tile's contraction
+  uint32_t steps_per_split = 1;
   int64_t groups = 0;
-  int64_t bytes() const { return 0; }
+  bool direct = false;           // dy is read where it lies
+  int64_t planes = 0;            // bytes of dy as bfloat16 planes in the workspace
+  int64_t parts = 0;             // bytes of the splits' sums
+  int64_t bytes() const { return planes + parts; }
 };
 GradPlan plan_grad(const reshard_matrix_t& dy, const reshard_matrix_t& x, const reshard_matrix_t& dw);
 hipError_t launch_grad(const GradPlan& plan, const reshard_matrix_t& dy, const reshard_matrix_t& x,

@@ -177,6 +177,8 @@ reshard_status_t check_grad(const reshard_matrix_t* dy, const reshard_matrix_t* 
   if (dy->rows != x->rows) return report(RESHARD_ERR_INVALID_ARGUMENT, "dy and x differ in rows (the contraction)");
   if (dw->rows != dy->cols || dw->cols != x->cols)
     return report(RESHARD_ERR_INVALID_ARGUMENT, "dw is not (columns of dy) x (columns of x)");
+  if (dy->cols > rs::kMaxGradCols || dy->rows * rs::grad_planes(dy->dtype) > rs::kMaxGradRows)
+    return bad("dy", "too many rows or columns for a weight gradient");
   if (rs::plan_grad(*dy, *x, *dw).groups > rs::kMaxGroups) return too_many();
   return RESHARD_OK;
 }

@@ -600,7 +600,8 @@ reshard_status_t reshard_block_matmul(const reshard_matrix_t* a, const reshard_m
                                       void* stream);
 
 /* Bytes of workspace reshard_block_matmul needs for matrices of these shapes and
- * types (data and scales are not looked at and may be NULL).  Host only. */
+ * types.  Host only: of the pointers only data's alignment matters, and NULL stands
+ * for an aligned one. */
 reshard_status_t reshard_block_matmul_workspace(const reshard_matrix_t* a, const reshard_matrix_t* b,
                                                 const reshard_matrix_t* out, int64_t* bytes);
 
@@ -613,7 +614,8 @@ reshard_status_t reshard_block_matmul_workspace(const reshard_matrix_t* a, const
  * that add up to it, each multiplied exactly; sums are held in binary32 (terms
  * that stay below 2^-126, where the matrix instructions have no bits, may be
  * lost).  An infinite dy or x gives an infinity or a NaN.  dw is plain.
- * workspace: as for reshard_block_matmul, of reshard_block_grad_workspace bytes.
+ * dy has at most 2^24 columns and 2^29 rows.  workspace: as for
+ * reshard_block_matmul, of reshard_block_grad_workspace bytes.
  */
 reshard_status_t reshard_block_grad(const reshard_matrix_t* dy, const reshard_matrix_t* x,
                                     const reshard_matrix_t* dw, int accumulate, void* workspace,

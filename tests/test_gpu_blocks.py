@@ -347,6 +347,22 @@ def test_grad_of_the_weight(mnk, dy_type, dw_type):
         check_product(dw.view, want, mass, terms, DTYPES[dw_type], False)
 
 
+@pytest.mark.parametrize("dy_type,fmt", [("bf16", E4M3), ("bf16", E5M2), ("f32", E4M3)])
+@pytest.mark.parametrize("mnk", [(200, 24600, 300), (129, 2056, 6001), (64, 6000, 2100), (1000, 8200, 1500)], ids=str)
+def test_grad_of_many_tiles(mnk, dy_type, fmt):
+    """Enough columns for the largest tiles; the 64-bit product on the GPU."""
+    m, n, k = mnk
+    g = values_of((m, n), "normal", m + k, torch.float32).to(DTYPES[dy_type])
+    dy = Plain(m, n, DTYPES[dy_type], value=g)
+    x = quantized(values_of((m, k), "normal", m + n, torch.float32), 1, fmt, extra=16, extra_scales=1)
+    dw = Plain(n, k, torch.float32, stride=k + 1, offset=1)
+    grad(dy, x.m, dw)
+    gv, xv = g.cuda().double(), torch.from_numpy(x.values()).cuda()
+    want, mass = gv.t().contiguous() @ xv, gv.abs().t().contiguous() @ xv.abs()
+    tol = m * (3 if dy_type == "f32" else 1) * 2.0 ** -24 * mass + 2.0 ** -24 * want.abs()
+    assert bool(((dw.view.double() - want).abs() <= tol + 1e-38).all())
+
+
 @pytest.mark.parametrize("dw_type", list(DTYPES))
 @pytest.mark.parametrize("mnk", [(40, 70, 200), (700, 130, 130), (0, 40, 200)], ids=str)
 def test_grad_accumulates(mnk, dw_type):
