@@ -17,6 +17,13 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
+// Workgroup `id` of `n` by the order in which workgroups go to the 8 XCDs in turn,
+// so that each XCD takes a contiguous run.
+__device__ __forceinline__ uint32_t run_of(uint32_t id, uint32_t n) {
+  const uint32_t xcd = id % 8;
+  return xcd * (n / 8) + min(xcd, n % 8) + id / 8;
+}
+
 // Keeps a value in registers at this point of the program: no use of it moves
 // above, no computation of it below.
 template <typename T> __device__ __forceinline__ void pin(T& x) {
@@ -68,6 +75,22 @@ template <typename T, int N> __device__ __forceinline__ Pack<T, N> load_pack(con
 }
 template <typename T, int N> __device__ __forceinline__ void store_pack(T* p, const Pack<T, N>& r) {
   __builtin_memcpy(p, &r, sizeof(r));
+}
+
+// A store past the caches, for what is not read again soon.
+template <int B> struct Words;
+template <> struct Words<4> { typedef uint32_t type __attribute__((aligned(1))); };
+template <> struct Words<8> { typedef uint32_t type __attribute__((ext_vector_type(2), aligned(1))); };
+template <> struct Words<16> { typedef uint32_t type __attribute__((ext_vector_type(4), aligned(1))); };
+template <typename T, int N> __device__ __forceinline__ void store_stream(T* p, const Pack<T, N>& r) {
+  constexpr int B = sizeof(T) * N > 16 ? 16 : sizeof(T) * N;
+  typedef typename Words<B>::type W;
+#pragma unroll
+  for (int i = 0; i < int(sizeof(T)) * N / B; ++i) {
+    W w;
+    __builtin_memcpy(&w, reinterpret_cast<const char*>(&r) + i * B, B);
+    __builtin_nontemporal_store(w, reinterpret_cast<W*>(p) + i);
+  }
 }
 
 // 2^(b - 127) of a scale byte (255: NaN, 0: the subnormal 2^-127).

@@ -118,8 +118,7 @@ __global__ __launch_bounds__(64 * WN * WK, 2) void grad_tiles(Output dy, Checkpo
   const int wn = wave / WK, wk = wave % WK;
   // tiles to XCDs in contiguous runs, whose tiles share operands in its L2
   const uint32_t split = blockIdx.x / tiles, id = blockIdx.x % tiles;
-  const uint32_t xcd = id % 8, per = tiles / 8, extra = tiles % 8;
-  const uint32_t t = xcd * per + min(xcd, extra) + id / 8;
+  const uint32_t t = run_of(id, tiles);
   const int n0 = int(t / k_tiles) * BN, k0 = int(t % k_tiles) * BK;
   const uint32_t all = uint32_t((rows + kDepth - 1) / kDepth);
   const uint32_t first = split * steps_per_split, last = min(first + steps_per_split, all);

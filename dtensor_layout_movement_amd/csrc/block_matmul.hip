@@ -164,9 +164,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tiles(Operand a, Opera
   const int wm = wave / WN, wn = wave % WN;
   // tiles to XCDs: each takes a contiguous run of tiles, rows of tiles fastest,
   // so that the tiles in flight on one share their operands in its L2
-  const uint32_t total = m_tiles * n_tiles, xcd = blockIdx.x % 8, at = blockIdx.x / 8;
-  const uint32_t per = total / 8, extra = total % 8;
-  const uint32_t t = xcd * per + min(xcd, extra) + at;
+  const uint32_t t = run_of(blockIdx.x, m_tiles * n_tiles);
   const int m0 = int(t % m_tiles) * BM, n0 = int(t / m_tiles) * BN;
 
   uint32_t off_a[BM * 8 / kThreads], off_b[BN * 8 / kThreads];
