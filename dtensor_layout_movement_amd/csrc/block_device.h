@@ -137,6 +137,36 @@ template <bool E5M2> __device__ __forceinline__ uint32_t quantize4(float a, floa
   return uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(c * inv, d * inv, r, true));
 }
 
+// N elements of a row from column c on as binary32, zero past `cols`.
+template <int DT, int N>
+__device__ __forceinline__ void load_up(const typename Elem<DT>::type* p, int c, int cols, float* x) {
+  typedef typename Elem<DT>::type T;
+  if (c + N <= cols) {
+    const Pack<T, N> v = load_pack<T, N>(p + c);
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = Elem<DT>::up(v.v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = c + i < cols ? Elem<DT>::up(p[c + i]) : 0.f;
+  }
+}
+
+// The largest of 16 neighbouring lanes, in all of them.
+template <int CTRL> __device__ __forceinline__ uint32_t max_with(uint32_t v) {
+  return max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), CTRL, 0xf, 0xf, true)));
+}
+__device__ __forceinline__ uint32_t max_of_16(uint32_t v) {
+  v = max_with<0xb1>(v);      // lane ^ 1
+  v = max_with<0x4e>(v);      // lane ^ 2
+  v = max_with<0x141>(v);     // 7 - lane of 8
+  return max_with<0x140>(v);  // 15 - lane of 16
+}
+
+// Eight elements as payload bytes.
+template <bool E5M2> __device__ __forceinline__ i32x2 quantize8(const float* x, float inv) {
+  return i32x2{int(quantize4<E5M2>(x[0], x[1], x[2], x[3], inv)), int(quantize4<E5M2>(x[4], x[5], x[6], x[7], inv))};
+}
+
 // Four 8-bit elements as binary32 (exact).
 template <bool E5M2> __device__ __forceinline__ f32x4 widen4(uint32_t q) {
   f32x4 r;

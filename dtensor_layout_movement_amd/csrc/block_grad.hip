@@ -100,28 +100,20 @@ __device__ __forceinline__ bf16x8 fragment(const uint8_t* p, int half) {
   return __builtin_bit_cast(bf16x8, s16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]});
 }
 
-// A workgroup makes a BN (columns of dy) x BK (columns of x) tile of dw with
-// WN x WK waves over the steps [first, last) of the contraction.  The next step's
-// dy goes straight to LDS and its x to registers while this step is multiplied;
-// x is then widened and put into the other buffer.
+// One BN (columns of dy, from n0) x BK (columns of x, from k0) tile of dw with
+// WN x WK waves over the steps [first, last) of the contraction, within the
+// caller's LDS, two buffers of kDepth * (BN + BK) * 2 bytes.  The next step's dy goes
+// straight to LDS and its x to registers while this step is multiplied; x is then
+// widened and put into the other buffer.
 template <int DT_W, bool E5M2, int BN, int BK, int WN, int WK>
-__global__ __launch_bounds__(64 * WN * WK, 2) void grad_tiles(Output dy, Checkpoint x, int rows, uint32_t k_tiles,
-                                                              uint32_t tiles, uint32_t steps_per_split,
-                                                              typename Elem<DT_W>::type* dw, int64_t dw_stride,
-                                                              int64_t split_stride, int accumulate) {
+__device__ __forceinline__ void make_tile(const Output& dy, const Checkpoint& x, int rows, int n0, int k0,
+                                          uint32_t first, uint32_t last, typename Elem<DT_W>::type* base,
+                                          int64_t dw_stride, int accumulate, uint8_t* tile0, uint8_t* tile1) {
   constexpr int kThreads = 64 * WN * WK, kN = BN / WN / 16, kK = BK / WK / 16;
   constexpr int kRowY = BN * 2, kRowX = BK * 2;  // bytes of a row in LDS
   constexpr int kLoadsY = kDepth * kRowY / 16 / kThreads, kLoadsX = kDepth * BK / 16 / kThreads;
-  __shared__ __align__(128) uint8_t tile0[kDepth * (kRowY + kRowX)];
-  __shared__ __align__(128) uint8_t tile1[kDepth * (kRowY + kRowX)];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wn = wave / WK, wk = wave % WK;
-  // tiles to XCDs in contiguous runs, whose tiles share operands in its L2
-  const uint32_t split = blockIdx.x / tiles, id = blockIdx.x % tiles;
-  const uint32_t t = run_of(id, tiles);
-  const int n0 = int(t / k_tiles) * BN, k0 = int(t % k_tiles) * BK;
-  const uint32_t all = uint32_t((rows + kDepth - 1) / kDepth);
-  const uint32_t first = split * steps_per_split, last = min(first + steps_per_split, all);
 
   // Where a lane's loads come from, within the step's rows.  Its loads of dy lie
   // kRowsY rows apart, a multiple of 16, so that their columns are the same.
@@ -239,7 +231,6 @@ __global__ __launch_bounds__(64 * WN * WK, 2) void grad_tiles(Output dy, Checkpo
     step(tile0);
   }
 
-  typename Elem<DT_W>::type* base = dw + split * split_stride;
 #pragma unroll
   for (int j = 0; j < kN; ++j) {
     const int n = n0 + (wn * kN + j) * 16 + (lane & 15);
@@ -265,6 +256,31 @@ __global__ __launch_bounds__(64 * WN * WK, 2) void grad_tiles(Output dy, Checkpo
   }
 }
 
+// A tile a workgroup, or a tile's split.  Workgroups from `whole` on, which would
+// leave half of the card idle in the last round, share a tile between two.
+template <int DT_W, bool E5M2, int B, int WN, int WK>
+__global__ __launch_bounds__(64 * WN * WK, 2) void grad_tiles(Output dy, Checkpoint x, int rows, uint32_t k_tiles,
+                                                              uint32_t tiles, uint32_t whole, uint32_t steps_per_split,
+                                                              typename Elem<DT_W>::type* dw, int64_t dw_stride,
+                                                              int64_t split_stride, int accumulate) {
+  __shared__ __align__(128) uint8_t tile0[kDepth * 4 * B];
+  __shared__ __align__(128) uint8_t tile1[kDepth * 4 * B];
+  const uint32_t all = uint32_t((rows + kDepth - 1) / kDepth);
+  if (blockIdx.x < whole) {
+    // tiles to XCDs in contiguous runs, whose tiles share operands in its L2
+    const uint32_t split = blockIdx.x / tiles, t = run_of(blockIdx.x % tiles, min(whole, tiles));
+    const uint32_t first = split * steps_per_split, last = min(first + steps_per_split, all);
+    make_tile<DT_W, E5M2, B, B, WN, WK>(dy, x, rows, int(t / k_tiles) * B, int(t % k_tiles) * B, first, last,
+                                        dw + split * split_stride, dw_stride, accumulate, tile0, tile1);
+  } else if constexpr (B == 256) {  // (one split)
+    const uint32_t half = run_of(blockIdx.x - whole, gridDim.x - whole), t = whole + half / 2;
+    const int k0 = int(t % k_tiles) * B + int(half % 2) * (B / 2);
+    if (k0 < x.cols)
+      make_tile<DT_W, E5M2, B, B / 2, 4, 2>(dy, x, rows, int(t / k_tiles) * B, k0, 0, all, dw, dw_stride, accumulate,
+                                            tile0, tile1);
+  }
+}
+
 template <int DT_W, bool E5M2>
 hipError_t grad_as(const GradPlan& plan, const Output& dy, const Checkpoint& c, int rows, void* dw, int64_t dw_stride,
                    int64_t split_stride, int accumulate, hipStream_t stream) {
@@ -272,11 +288,11 @@ hipError_t grad_as(const GradPlan& plan, const Output& dy, const Checkpoint& c, 
   const uint32_t k_tiles = uint32_t(ceil_div(c.cols, plan.tile));
   const uint32_t tiles = k_tiles * uint32_t(ceil_div(dy.cols, plan.tile));
   if (plan.tile == 256)
-    grad_tiles<DT_W, E5M2, 256, 256, 2, 4><<<dim3(uint32_t(plan.groups)), 512, 0, stream>>>(
-        dy, c, rows, k_tiles, tiles, plan.steps_per_split, static_cast<T*>(dw), dw_stride, split_stride, accumulate);
+    grad_tiles<DT_W, E5M2, 256, 2, 4><<<dim3(uint32_t(plan.groups)), 512, 0, stream>>>(
+        dy, c, rows, k_tiles, tiles, uint32_t(plan.whole), plan.steps_per_split, static_cast<T*>(dw), dw_stride, split_stride, accumulate);
   else
-    grad_tiles<DT_W, E5M2, 128, 128, 2, 2><<<dim3(uint32_t(plan.groups)), 256, 0, stream>>>(
-        dy, c, rows, k_tiles, tiles, plan.steps_per_split, static_cast<T*>(dw), dw_stride, split_stride, accumulate);
+    grad_tiles<DT_W, E5M2, 128, 2, 2><<<dim3(uint32_t(plan.groups)), 256, 0, stream>>>(
+        dy, c, rows, k_tiles, tiles, uint32_t(plan.whole), plan.steps_per_split, static_cast<T*>(dw), dw_stride, split_stride, accumulate);
   return hipGetLastError();
 }
 
@@ -351,7 +367,11 @@ GradPlan plan_grad(const reshard_matrix_t& dy, const reshard_matrix_t& x, const 
   p.steps_per_split = uint32_t(std::max<int64_t>(1, ceil_div(steps, splits)));
   splits = std::max<int64_t>(1, ceil_div(steps, p.steps_per_split));
   p.splits = int(splits);
-  p.groups = tiles * splits;
+  p.whole = p.groups = tiles * splits;
+  if (p.tile == 256) {
+    p.whole = whole_tiles(tiles);
+    p.groups = 2 * tiles - p.whole;
+  }
   // bf16 rows on the 16-byte grid are read where they lie
   p.direct = dy.dtype == RESHARD_DTYPE_BF16 && dy.row_stride % 8 == 0 && dy.row_stride <= kMaxGradCols &&
              reinterpret_cast<uintptr_t>(dy.data) % 16 == 0;

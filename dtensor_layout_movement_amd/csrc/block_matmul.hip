@@ -2,6 +2,8 @@
 #include "block_device.h"
 #include "blocks.h"
 
+#include <algorithm>
+
 namespace rs {
 namespace {
 
@@ -31,12 +33,14 @@ Operand operand(const reshard_matrix_t& m) {
 // instructions, whose products and sums lose nothing above binary32's
 // rounding (8e-8 in the same test).  Each lane holds 32 consecutive elements of
 // its row, on both sides, so the order within the step is the same for both.
-template <bool EXACT, bool E5_1, bool E5_2>
+//
+// A scale is byte BX (BY) of the word that holds it.
+template <bool EXACT, bool E5_1, bool E5_2, int BX = 0, int BY = 0>
 __device__ __forceinline__ f32x4 step128(const i32x8& x, uint32_t sx, const i32x8& y, uint32_t sy, f32x4 acc) {
   if (!EXACT)
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, acc, E5_1 ? 1 : 0, E5_2 ? 1 : 0, 0, int(sx), 0,
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, acc, E5_1 ? 1 : 0, E5_2 ? 1 : 0, BX, int(sx), BY,
                                                             int(sy));
-  const float fx = scale_value(sx), fy = scale_value(sy);
+  const float fx = scale_value(sx >> (8 * BX) & 255), fy = scale_value(sy >> (8 * BY) & 255);
 #pragma unroll
   for (int k = 0; k < 4; ++k)
     acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8_bf16<E5_1>(uint32_t(x[2 * k]), uint32_t(x[2 * k + 1]), fx),
@@ -45,61 +49,132 @@ __device__ __forceinline__ f32x4 step128(const i32x8& x, uint32_t sx, const i32x
   return acc;
 }
 
+// Four neighbouring results, of which `left` are inside the row.
+template <int DT>
+__device__ __forceinline__ void store4(typename Elem<DT>::type* p, const f32x4& v, int left) {
+  Pack<typename Elem<DT>::type, 4> r;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) r.v[e] = Elem<DT>::down(v[e]);
+  if (left >= 4) {
+    store_pack<typename Elem<DT>::type, 4>(p, r);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < left) p[e] = r.v[e];
+  }
+}
+
+// A lane's 32 bytes of a row's 128: pieces `part` and `part` + 4 of 16 bytes, so that
+// four lanes read 64 neighbouring bytes at a time (the order within a step only
+// has to be the same on both sides).
 __device__ __forceinline__ i32x8 load32(const uint8_t* p) {
-  const i32x4 a = reinterpret_cast<const i32x4*>(p)[0], b = reinterpret_cast<const i32x4*>(p)[1];
+  const i32x4 a = reinterpret_cast<const i32x4*>(p)[0], b = reinterpret_cast<const i32x4*>(p)[4];
   return i32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
 
-// The simple form, for any shape: a workgroup makes a 16 (columns of out) x
-// 16 * MT (rows) tile; its four waves share the contraction and join their sums
-// through LDS in wave order.  The weight's rows are the instruction's first
-// operand, so that a lane ends with four neighbouring columns of one row of out.
-constexpr int kWaves = 4;
+// Up to kMaxRowsForm rows of a.  A workgroup makes 16 columns of out; its waves
+// share the contraction, block by block in turn, and their sums are joined through
+// LDS in wave order.  Bound by the weight's bytes: each wave has the loads of
+// kAhead blocks under way at once, and the waves of a workgroup are as many as it
+// takes to fill the card (rows_waves).  The weight's rows are the instruction's
+// first operand, so that a lane ends with four neighbouring columns of one row of
+// out.  With more rows the loads of a, which every workgroup makes, cost more than
+// the ring's trip through LDS.
+//
+// SRC: the type of a plain a of few elements (kFusedBytes), which each workgroup
+// quantizes for itself into LDS while its first weights are on their way; 0: a is
+// held.
+constexpr int64_t kMaxRowsForm = 4;
+constexpr int kFusedBytes = 16384;  // payload bytes in LDS
+constexpr int kFusedPad = 16;       // between rows there: rows start in distinct banks
+constexpr int kMaxWaves = 16;
 
-template <int DT, bool E5_A, bool E5_B, int MT>
-__global__ __launch_bounds__(64 * kWaves) void matmul_rows(Operand a, Operand b, uint32_t blocks, uint32_t n_tiles,
-                                                           typename Elem<DT>::type* out, int64_t out_stride) {
+template <int DT, bool E5_A, bool E5_B, int SRC>
+__global__ __launch_bounds__(64 * kMaxWaves) void matmul_rows(Operand a, Operand b, int cols, uint32_t blocks,
+                                                              typename Elem<DT>::type* out, int64_t out_stride) {
   constexpr bool kExact = DT == RESHARD_DTYPE_F32;
-  __shared__ f32x4 sums[kWaves - 1][MT][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int n0 = int(blockIdx.x % n_tiles) * 16, m0 = int(blockIdx.x / n_tiles) * (16 * MT);
-  const int part = lane >> 4;
-  const int rb = min(n0 + (lane & 15), b.rows - 1);
-  const uint8_t* pb = b.data + rb * b.stride + part * 32;
+  constexpr int kAhead = 4;
+  extern __shared__ __align__(16) uint8_t lds[];  // sums of all waves, then a's payload and scales
+  f32x4* sums = reinterpret_cast<f32x4*>(lds);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t waves = blockDim.x >> 6;
+  const int n0 = int(run_of(blockIdx.x, gridDim.x)) * 16, part = lane >> 4;
+  const int rb = min(n0 + (lane & 15), b.rows - 1), ra = min(lane & 15, a.rows - 1);
+  const uint8_t* pb = b.data + rb * b.stride + part * 16;
   const uint8_t* sb = b.scales + int64_t(rb >> b.row_shift) * b.scale_stride;
-  const uint8_t* pa[MT];
-  const uint8_t* sa[MT];
-  f32x4 acc[MT];
+
+  i32x8 x[kAhead];
+  uint32_t sx[kAhead];
+  const auto load_b = [&](uint32_t k) {
 #pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    const int ra = min(m0 + 16 * t + (lane & 15), a.rows - 1);
-    pa[t] = a.data + ra * a.stride + part * 32;
-    sa[t] = a.scales + int64_t(ra >> a.row_shift) * a.scale_stride;
-    acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
-  for (uint32_t k = wave; k < blocks; k += kWaves) {
-    const i32x8 x = load32(pb + int64_t(k) * kBlock);
-    const uint32_t sx = sb[k];
+    for (int u = 0; u < kAhead; ++u) {
+      const uint32_t at = min(k + u * waves, blocks - 1);
+      x[u] = load32(pb + int64_t(at) * kBlock);
+      sx[u] = sb[at];
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  if (blocks) load_b(wave);  // (an empty contraction has nothing to read)
+
+  const uint8_t *pa, *sa;
+  if constexpr (SRC != 0) {
+    typedef typename Elem<SRC>::type S;
+    uint8_t* payload = lds + waves * (64 * sizeof(f32x4));
+    const int stride = int(blocks) * kBlock + kFusedPad;
+    uint8_t* scales = payload + a.rows * stride;
+    const int sixteenth = threadIdx.x & 15;
+    for (uint32_t i = threadIdx.x >> 4; i < a.rows * blocks; i += blockDim.x >> 4) {
+      const uint32_t row = i / blocks, block = i - row * blocks;
+      float v[8];
+      load_up<SRC, 8>(reinterpret_cast<const S*>(a.data) + row * a.stride, int(block) * kBlock + sixteenth * 8, cols, v);
+      uint32_t amax = 0;
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
-      acc[t] = step128<kExact, E5_B, E5_A>(x, sx, load32(pa[t] + int64_t(k) * kBlock), sa[t][k], acc[t]);
+      for (int e = 0; e < 8; ++e) amax = max(amax, finite_magnitude(v[e]));
+      const uint32_t s = scale_byte<false>(max_of_16(amax));
+      *reinterpret_cast<i32x2*>(payload + row * stride + block * kBlock + sixteenth * 8) =
+          quantize8<false>(v, inverse_scale(s));
+      if (sixteenth == 0) scales[i] = uint8_t(s);
+    }
+    __syncthreads();
+    pa = payload + ra * stride + part * 16;
+    sa = scales + ra * int(blocks);
+  } else {
+    pa = a.data + ra * a.stride + part * 16;
+    sa = a.scales + int64_t(ra >> a.row_shift) * a.scale_stride;
   }
-  if (wave) {
+
+  f32x4 acc{0.f, 0.f, 0.f, 0.f};
+  for (uint32_t k = wave; k < blocks; k += kAhead * waves) {
+    i32x8 y[kAhead];
+    uint32_t sy[kAhead];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) sums[wave - 1][t][lane] = acc[t];
+    for (int u = 0; u < kAhead; ++u) {
+      const uint32_t at = min(k + u * waves, blocks - 1);
+      y[u] = load32(pa + int64_t(at) * kBlock);
+      sy[u] = sa[at];
+    }
+    __builtin_amdgcn_sched_barrier(0);  // all loads first
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (k + u * waves >= blocks) break;
+      acc = step128<kExact, E5_B, E5_A>(x[u], sx[u], y[u], sy[u], acc);
+    }
+    if (k + kAhead * waves < blocks) load_b(k + kAhead * waves);
   }
+  sums[wave * 64 + lane] = acc;
   __syncthreads();
   if (wave) return;
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-#pragma unroll
-    for (int w = 0; w < kWaves - 1; ++w) acc[t] += sums[w][t][lane];
-    const int m = m0 + 16 * t + (lane & 15), n = n0 + part * 4;
-    if (m >= a.rows) continue;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (n + i < b.rows) out[m * out_stride + n + i] = Elem<DT>::down(acc[t][i]);
-  }
+  for (uint32_t w = 1; w < waves; ++w) acc += sums[w * 64 + lane];
+  const int m = lane & 15, n = n0 + part * 4;
+  if (m < a.rows) store4<DT>(out + m * out_stride + n, acc, b.rows - n);
+}
+
+// Waves of a workgroup: as many as bring 4096 of them onto the card, at most one a
+// block of the contraction.
+int rows_waves(int64_t groups, int64_t blocks) {
+  int w = 4;
+  while (w < kMaxWaves && groups * w < 4096 && w < blocks) w *= 2;
+  return w;
 }
 
 // The tiled form.  A workgroup makes a BM (rows of a) x BN (rows of b) tile with
@@ -151,22 +226,28 @@ __device__ __forceinline__ uint32_t load_scales(const uint8_t* row, uint32_t k, 
   return v;
 }
 
+constexpr uint32_t kBand = 8;
+
+template <int N> struct Index {
+  static constexpr int value = N;
+};
+template <int N, typename F> __device__ __forceinline__ void for_each_index(F f) {
+  if constexpr (N > 0) {
+    for_each_index<N - 1>(f);
+    f(Index<N - 1>{});
+  }
+}
+
+// One tile, rows from m0 and columns from n0 on, within the caller's LDS: two
+// buffers of (BM + BN) * 128 bytes and the scales of eight steps.
 template <int DT, bool E5_A, bool E5_B, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tiles(Operand a, Operand b, uint32_t blocks, uint32_t m_tiles,
-                                                                uint32_t n_tiles, typename Elem<DT>::type* out,
-                                                                int64_t out_stride) {
+__device__ __forceinline__ void make_tile(const Operand& a, const Operand& b, uint32_t blocks, int m0, int n0,
+                                          typename Elem<DT>::type* out, int64_t out_stride, uint8_t* tile0,
+                                          uint8_t* tile1, uint8_t* scales) {
   constexpr bool kExact = DT == RESHARD_DTYPE_F32;
   constexpr int kThreads = 64 * WM * WN, kM = BM / WM / 16, kN = BN / WN / 16;
-  __shared__ __align__(128) uint8_t tile0[(BM + BN) * kBlock];
-  __shared__ __align__(128) uint8_t tile1[(BM + BN) * kBlock];
-  __shared__ uint32_t scales[2][BM + BN];  // four steps of every row, two groups of steps
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
-  // tiles to XCDs: each takes a contiguous run of tiles, rows of tiles fastest,
-  // so that the tiles in flight on one share their operands in its L2
-  const uint32_t t = run_of(blockIdx.x, m_tiles * n_tiles);
-  const int m0 = int(t % m_tiles) * BM, n0 = int(t / m_tiles) * BN;
-
   uint32_t off_a[BM * 8 / kThreads], off_b[BN * 8 / kThreads];
   stage_offsets<BM, kThreads>(a, m0, off_a);
   stage_offsets<BN, kThreads>(b, n0, off_b);
@@ -186,6 +267,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tiles(Operand a, Opera
     else
       srow[i] = b.scales + int64_t(min(n0 + r - BM, b.rows - 1) >> b.row_shift) * b.scale_stride;
   }
+  // Within a step's scales the rows of a lane in all fragments of its wave lie
+  // together, so that one read gives a lane four of them, which the instruction
+  // selects from.
+  const auto scale_place = [](int r) {  // row r = (wave row, fragment, lane row)
+    if (r < BM) return r / (16 * kM) * (16 * kM) + r % 16 * kM + r / 16 % kM;
+    const int q = r - BM;
+    return BM + q / (16 * kN) * (16 * kN) + q % 16 * kN + q / 16 % kN;
+  };
+  static_assert(kM % 4 == 0 && kN % 4 == 0, "four scales a word");
   uint32_t held_scales[kScaleRows];
   const auto load_scale_group = [&](uint32_t k) {
 #pragma unroll
@@ -195,7 +285,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tiles(Operand a, Opera
 #pragma unroll
     for (int i = 0; i < kScaleRows; ++i) {
       const int r = int(threadIdx.x) + i * kThreads;
-      if (r < BM + BN) scales[(k >> 2) & 1][r] = held_scales[i];
+      if (r < BM + BN)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) scales[((k + e) & 7) * (BM + BN) + scale_place(r)] = uint8_t(held_scales[i] >> (8 * e));
     }
   };
 
@@ -207,65 +299,87 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tiles(Operand a, Opera
 
   const int frow = lane & 15, part = lane >> 4;
   // where this lane's fragments lie in a tile: rows 16 apart keep their slots
-  const int slot0 = slot_of(frow, 2 * part) * 16, slot1 = slot_of(frow, 2 * part + 1) * 16;
+  const int slot0 = slot_of(frow, part) * 16, slot1 = slot_of(frow, part + 4) * 16;
   const int row_a = (wm * (BM / WM) + frow), row_b = BM + wn * (BN / WN) + frow;
-  const uint8_t* scale_bytes = reinterpret_cast<const uint8_t*>(scales);
-  const auto step = [&](const uint8_t* tile, uint32_t k) {
-    const uint8_t* sk = scale_bytes + ((k >> 2) & 1) * ((BM + BN) * 4) + (k & 3);
-    const uint8_t *a0 = tile + row_a * kBlock + slot0, *a1 = tile + row_a * kBlock + slot1;
-    const uint8_t *b0 = tile + row_b * kBlock + slot0, *b1 = tile + row_b * kBlock + slot1;
-    i32x8 y[kN];
-    uint32_t sb[kN];
+  // b's fragments of a step and the first of a's, read before the step begins
+  i32x8 x, y[kN];
+  uint32_t sa[kM / 4], sb[kN / 4];
+  const auto begin = [&](const uint8_t* tile, uint32_t k) {
+    const uint8_t* sk = scales + (k & 7) * (BM + BN);
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      y[i] = fragment(b0, b1, i * 16 * kBlock);
-      sb[i] = sk[row_b * 4 + i * 64];
-    }
-    // one fragment of a ahead of its products; the pins keep the compiler from
-    // reading all of them first, which does not fit the registers
-    i32x8 x = fragment(a0, a1, 0);
-    uint32_t sa = sk[row_a * 4];
-#pragma unroll
-    for (int j = 0; j < kM; ++j) {
-      i32x8 next = x;
-      uint32_t snext = sa;
-      if (j + 1 < kM) {
-        next = fragment(a0, a1, (j + 1) * 16 * kBlock);
-        snext = sk[row_a * 4 + (j + 1) * 64];
-      }
-#pragma unroll
-      for (int i = 0; i < kN; ++i) {
-        acc[i][j] = step128<kExact, E5_B, E5_A>(y[i], sb[i], x, sa, acc[i][j]);
-        pin(acc[i][j]);
-      }
-      __builtin_amdgcn_sched_barrier(0);
+    for (int i = 0; i < kN; ++i)
+      y[i] = fragment(tile + row_b * kBlock + slot0, tile + row_b * kBlock + slot1, i * 16 * kBlock);
+    x = fragment(tile + row_a * kBlock + slot0, tile + row_a * kBlock + slot1, 0);
+    __builtin_memcpy(sa, __builtin_assume_aligned(sk + wm * (16 * kM) + frow * kM, kM), kM);
+    __builtin_memcpy(sb, __builtin_assume_aligned(sk + BM + wn * (16 * kN) + frow * kN, kN), kN);
+  };
+  // Step k, then what `turn` does between the step's last LDS read and its last
+  // products: those hide the barrier and the next step's first reads.  One
+  // fragment of a is read ahead of its products; the pins keep the compiler from
+  // reading all of them first, which does not fit the registers.
+  const auto products = [&](auto J, const i32x8 (&yj)[kN], const uint32_t (&sbj)[kN / 4], const i32x8& xj,
+                            const uint32_t (&saj)[kM / 4]) {
+    constexpr int j = decltype(J)::value;
+    for_each_index<kN>([&](auto I) {
+      constexpr int i = decltype(I)::value;
+      acc[i][j] = step128<kExact, E5_B, E5_A, i % 4, j % 4>(yj[i], sbj[i / 4], xj, saj[j / 4], acc[i][j]);
+      pin(acc[i][j]);
+    });
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  const auto step = [&](const uint8_t* tile, auto turn) {
+    const auto fragment_a = [&](int j) {
+      return fragment(tile + row_a * kBlock + slot0, tile + row_a * kBlock + slot1, j * 16 * kBlock);
+    };
+    i32x8 next = fragment_a(1);
+    for_each_index<kM - 2>([&](auto J) {
+      const i32x8 second = fragment_a(decltype(J)::value + 2);
+      products(J, y, sb, x, sa);
       x = next;
-      sa = snext;
-    }
+      next = second;
+    });
+    const i32x8 xl = x;
+    i32x8 yl[kN];
+    uint32_t sal[kM / 4], sbl[kN / 4];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) yl[i] = y[i];
+#pragma unroll
+    for (int i = 0; i < kN / 4; ++i) sbl[i] = sb[i];
+#pragma unroll
+    for (int j = 0; j < kM / 4; ++j) sal[j] = sa[j];
+    turn();
+    products(Index<kM - 2>{}, yl, sbl, xl, sal);
+    products(Index<kM - 1>{}, yl, sbl, next, sal);
   };
 
   if (blocks) {
     load(tile0, 0);
     load_scale_group(0);
     store_scale_group(0);
+    __syncthreads();
+    if (blocks > 1) load(tile1, 1);
+    begin(tile0, 0);
   }
+  // The next four steps' scales are loaded in one step and put down in the next,
+  // into the group that was last read four steps ago.
   for (uint32_t k = 0; k + 1 < blocks; k += 2) {
-    __syncthreads();  // tile0 has arrived, tile1 is free
-    load(tile1, k + 1);
-    // the next four steps' scales: loaded in one step, put down in the next,
-    // into the group that was last read four steps ago
-    const bool scale_turn = (k & 2) == 0 && k + 4 < blocks;
+    const bool scale_turn = (k & 2) == 0 && k + 4 < blocks, more = k + 2 < blocks;
     if (scale_turn) load_scale_group(k + 4);
-    step(tile0, k);
-    __syncthreads();
-    if (k + 2 < blocks) load(tile0, k + 2);
-    if (scale_turn) store_scale_group(k + 4);
-    step(tile1, k + 1);
+    step(tile0, [&] {
+      __syncthreads();  // tile1 has arrived, tile0 has been read
+      begin(tile1, k + 1);
+      if (more) load(tile0, k + 2);
+      if (scale_turn) store_scale_group(k + 4);
+    });
+    step(tile1, [&] {
+      __syncthreads();
+      if (more) {
+        begin(tile0, k + 2);
+        if (k + 3 < blocks) load(tile1, k + 3);
+      }
+    });
   }
-  if (blocks & 1) {
-    __syncthreads();
-    step(tile0, blocks - 1);
-  }
+  if (blocks & 1) step(tile0, [] {});
 #pragma unroll
   for (int j = 0; j < kM; ++j) {
     const int m = m0 + wm * (BM / WM) + j * 16 + frow;
@@ -274,74 +388,291 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tiles(Operand a, Opera
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       const int n = n0 + wn * (BN / WN) + i * 16 + part * 4;
-      Pack<typename Elem<DT>::type, 4> v;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v.v[e] = Elem<DT>::down(acc[i][j][e]);
-      if (n + 4 <= b.rows) {
-        store_pack<typename Elem<DT>::type, 4>(row + n, v);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (n + e < b.rows) row[n + e] = v.v[e];
-      }
+      store4<DT>(row + n, acc[i][j], b.rows - n);
     }
   }
 }
 
-constexpr int kMT = 4;
+// A tile a workgroup.  Workgroups from `whole` on, which would leave half of the
+// card idle in the last round, share a tile between two.
+template <int DT, bool E5_A, bool E5_B, int B, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tiles(Operand a, Operand b, uint32_t blocks, uint32_t m_tiles,
+                                                                uint32_t n_tiles, uint32_t whole,
+                                                                typename Elem<DT>::type* out, int64_t out_stride) {
+  __shared__ __align__(128) uint8_t tile0[2 * B * kBlock];
+  __shared__ __align__(128) uint8_t tile1[2 * B * kBlock];
+  __shared__ __align__(16) uint8_t scales[8 * 2 * B];
+  // Each XCD takes a contiguous run of tiles, in bands of kBand rows of tiles, so
+  // that what is in flight on one is nearly square and shares the most in its L2
+  // (8192^3: 505 -> 460 us).
+  const auto place = [&](uint32_t t, int* m0, int* n0) {
+    const uint32_t band = t / (kBand * n_tiles), rows = min(kBand, m_tiles - band * kBand), in = t - band * kBand * n_tiles;
+    *m0 = int(band * kBand + in % rows) * B;
+    *n0 = int(in / rows) * B;
+  };
+  int m0, n0;
+  if (blockIdx.x < whole) {
+    place(run_of(blockIdx.x, whole), &m0, &n0);
+    make_tile<DT, E5_A, E5_B, B, B, WM, WN>(a, b, blocks, m0, n0, out, out_stride, tile0, tile1, scales);
+  } else if constexpr (B == 256) {
+    const uint32_t half = run_of(blockIdx.x - whole, gridDim.x - whole);
+    place(whole + half / 2, &m0, &n0);
+    n0 += int(half % 2) * (B / 2);
+    if (n0 < b.rows)
+      make_tile<DT, E5_A, E5_B, B, B / 2, 4, 2>(a, b, blocks, m0, n0, out, out_stride, tile0, tile1, scales);
+  }
+}
+
+// The ring form, for products that do not fill the card with large tiles: a
+// workgroup of four waves makes a BM x 64 tile over the steps [first, last) of the
+// contraction.  Such products are bound by the latency of their loads, so four LDS
+// buffers keep three steps under way; a step waits for the oldest only.  The
+// scales of up to kChunk steps are put into LDS beforehand.  Where the tiles are
+// few, several workgroups share a contraction and write binary32 sums that
+// join_parts adds in order.
+constexpr int kRing = 4, kChunk = 64, kRingCols = 64;
+
+// Waits for all but `left` of this wave's loads to LDS and for its LDS reads, then
+// for the other waves.
+template <int LEFT> __device__ __forceinline__ void ring_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((LEFT & 15) | ((LEFT >> 4) << 14) | (7 << 4));
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+template <int DT, bool E5_A, bool E5_B, int MT, int WM, int OUT>
+__global__ __launch_bounds__(256) void matmul_ring(Operand a, Operand b, uint32_t blocks, uint32_t steps_per_split,
+                                                   uint32_t m_tiles, uint32_t tiles, typename Elem<OUT>::type* out,
+                                                   int64_t out_stride, int64_t split_stride) {
+  constexpr bool kExact = DT == RESHARD_DTYPE_F32;
+  constexpr int kThreads = 256, BM = 16 * MT, BN = kRingCols, WN = 4 / WM;
+  constexpr int kRowsA = BM < 32 ? 32 : BM;  // in LDS: a whole load a thread
+  constexpr int kM = MT / WM, kN = BN / WN / 16;
+  constexpr int kLoads = (kRowsA + BN) * 8 / kThreads;
+  __shared__ __align__(128) uint8_t ring0[(kRowsA + BN) * kBlock], ring1[(kRowsA + BN) * kBlock];
+  __shared__ __align__(128) uint8_t ring2[(kRowsA + BN) * kBlock], ring3[(kRowsA + BN) * kBlock];
+  __shared__ __align__(16) uint8_t scales[kChunk * (kRowsA + BN)];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const uint32_t split = blockIdx.x / tiles, t = run_of(blockIdx.x % tiles, tiles);
+  const int m0 = int(t % m_tiles) * BM, n0 = int(t / m_tiles) * BN;
+  const uint32_t first = split * steps_per_split, last = min(first + steps_per_split, blocks);
+
+  uint32_t off_a[kRowsA * 8 / kThreads], off_b[BN * 8 / kThreads];
+  stage_offsets<kRowsA, kThreads>(a, m0, off_a);
+  stage_offsets<BN, kThreads>(b, n0, off_b);
+  const Buffer base_a = rows_of(a, m0, kRowsA, blocks), base_b = rows_of(b, n0, BN, blocks);
+  const auto load = [&](uint8_t* to, uint32_t k) {
+    stage<kRowsA, kThreads>(base_a, off_a, k * kBlock, to, wave);
+    stage<BN, kThreads>(base_b, off_b, k * kBlock, to + kRowsA * kBlock, wave);
+  };
+
+  f32x4 acc[kN][kM];
+#pragma unroll
+  for (int i = 0; i < kN; ++i)
+#pragma unroll
+    for (int j = 0; j < kM; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int frow = lane & 15, part = lane >> 4;
+  const int slot0 = slot_of(frow, part) * 16, slot1 = slot_of(frow, part + 4) * 16;
+  const int row_a = wm * (BM / WM) + frow, row_b = kRowsA + wn * (BN / WN) + frow;
+  const auto step = [&](const uint8_t* tile, uint32_t s) {
+    const uint8_t* sk = scales + s * (kRowsA + BN);
+    i32x8 x[kM], y[kN];
+    uint32_t sa[kM], sb[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      y[i] = fragment(tile + row_b * kBlock + slot0, tile + row_b * kBlock + slot1, i * 16 * kBlock);
+      sb[i] = sk[row_b + i * 16];
+    }
+#pragma unroll
+    for (int j = 0; j < kM; ++j) {
+      x[j] = fragment(tile + row_a * kBlock + slot0, tile + row_a * kBlock + slot1, j * 16 * kBlock);
+      sa[j] = sk[row_a + j * 16];
+    }
+#pragma unroll
+    for (int j = 0; j < kM; ++j)
+#pragma unroll
+      for (int i = 0; i < kN; ++i) acc[i][j] = step128<kExact, E5_B, E5_A>(y[i], sb[i], x[j], sa[j], acc[i][j]);
+  };
+
+  for (uint32_t chunk = first; chunk < last; chunk += kChunk) {
+    const uint32_t steps = min(uint32_t(kChunk), last - chunk);
+    uint8_t* const ring[kRing] = {ring0, ring1, ring2, ring3};
+    __syncthreads();  // the last chunk's steps have been read
+#pragma unroll
+    for (int i = 0; i < kRing - 1; ++i) load(ring[i], chunk + min(uint32_t(i), steps - 1));
+    for (uint32_t i = threadIdx.x; i < (kRowsA + BN) * (kChunk / 4); i += kThreads) {
+      const uint32_t r = i / (kChunk / 4), g = i % (kChunk / 4) * 4;
+      if (g >= steps) continue;
+      const uint8_t* from =
+          r < kRowsA ? a.scales + int64_t(min(m0 + int(r), a.rows - 1) >> a.row_shift) * a.scale_stride
+                     : b.scales + int64_t(min(n0 + int(r) - kRowsA, b.rows - 1) >> b.row_shift) * b.scale_stride;
+      const uint32_t v = load_scales(from, chunk + g, blocks);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) scales[(g + e) * (kRowsA + BN) + r] = uint8_t(v >> (8 * e));
+    }
+    const uint32_t whole = steps / kRing * kRing;
+    for (uint32_t s = 0; s < whole; s += kRing) {
+#pragma unroll
+      for (int i = 0; i < kRing; ++i) {
+        // step s + i has arrived for every wave, and every wave is done with the
+        // step before it, whose buffer the next load takes; past the last step the
+        // loads go on (to no use), so that their count stays the same
+        ring_barrier<(kRing - 2) * kLoads>();
+        load(ring[(i + kRing - 1) % kRing], chunk + min(s + i + kRing - 1, steps - 1));
+        step(ring[i], s + i);
+      }
+    }
+    ring_barrier<0>();  // the last three steps have arrived; no load may outlive its use of LDS
+#pragma unroll
+    for (int i = 0; i < kRing - 1; ++i)
+      if (whole + i < steps) step(ring[i], whole + i);
+  }
+
+  typename Elem<OUT>::type* base = out + split * split_stride;
+#pragma unroll
+  for (int j = 0; j < kM; ++j) {
+    const int m = m0 + wm * (BM / WM) + j * 16 + frow;
+    if (m >= a.rows) continue;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int n = n0 + wn * (BN / WN) + i * 16 + part * 4;
+      store4<OUT>(base + m * out_stride + n, acc[i][j], b.rows - n);
+    }
+  }
+}
+
+template <int DT, bool E5_A, bool E5_B, int SRC>
+hipError_t rows_as(const MatmulPlan& plan, const reshard_matrix_t& a, const reshard_matrix_t& b,
+                   const reshard_matrix_t& out, hipStream_t stream) {
+  const uint32_t blocks = uint32_t(blocks_of(a.cols));
+  const int64_t fused = SRC ? a.rows * (int64_t(blocks) * (kBlock + 1) + kFusedPad) : 0;
+  matmul_rows<DT, E5_A, E5_B, SRC><<<dim3(uint32_t(plan.groups)), 64 * plan.waves,
+                                     uint32_t(plan.waves * 64 * sizeof(f32x4) + fused), stream>>>(
+      operand(a), operand(b), int(a.cols), blocks, static_cast<typename Elem<DT>::type*>(out.data), out.row_stride);
+  return hipGetLastError();
+}
+
+template <int DT, bool E5_A, bool E5_B, int B, int WM, int WN>
+hipError_t tiles_as(const MatmulPlan& plan, const reshard_matrix_t& a, const reshard_matrix_t& b,
+                    const reshard_matrix_t& out, hipStream_t stream) {
+  matmul_tiles<DT, E5_A, E5_B, B, WM, WN><<<dim3(uint32_t(plan.groups)), 64 * WM * WN, 0, stream>>>(
+      operand(a), operand(b), uint32_t(blocks_of(a.cols)), uint32_t(ceil_div(a.rows, B)), uint32_t(ceil_div(b.rows, B)),
+      uint32_t(plan.whole), static_cast<typename Elem<DT>::type*>(out.data), out.row_stride);
+  return hipGetLastError();
+}
+
+template <int DT, bool E5_A, bool E5_B, int MT, int WM>
+hipError_t ring_as(const MatmulPlan& plan, const reshard_matrix_t& a, const reshard_matrix_t& b,
+                   const reshard_matrix_t& out, void* workspace, hipStream_t stream) {
+  const uint32_t blocks = uint32_t(blocks_of(a.cols)), m_tiles = uint32_t(ceil_div(a.rows, 16 * MT));
+  const uint32_t tiles = m_tiles * uint32_t(ceil_div(b.rows, kRingCols));
+  const dim3 grid(uint32_t(plan.groups));
+  if (plan.splits == 1) {
+    matmul_ring<DT, E5_A, E5_B, MT, WM, DT><<<grid, 256, 0, stream>>>(
+        operand(a), operand(b), blocks, plan.steps_per_split, m_tiles, tiles,
+        static_cast<typename Elem<DT>::type*>(out.data), out.row_stride, 0);
+    return hipGetLastError();
+  }
+  float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.quantized + plan.quantized_scales);
+  const int64_t stride = round_up(out.cols, 4), size = out.rows * stride;
+  matmul_ring<DT, E5_A, E5_B, MT, WM, RESHARD_DTYPE_F32><<<grid, 256, 0, stream>>>(
+      operand(a), operand(b), blocks, plan.steps_per_split, m_tiles, tiles, parts, stride, size);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  return launch_join(parts, plan.splits, size, out, false, stream);
+}
 
 template <int DT, bool E5_A, bool E5_B>
 hipError_t matmul_as(const MatmulPlan& plan, const reshard_matrix_t& a, const reshard_matrix_t& b,
-                     const reshard_matrix_t& out, hipStream_t stream) {
-  typedef typename Elem<DT>::type T;
-  const uint32_t blocks = uint32_t(blocks_of(a.cols)), n_tiles = uint32_t(ceil_div(b.rows, 16));
-  if (plan.tile == 256) {
-    if constexpr (DT != RESHARD_DTYPE_F32)
-      matmul_tiles<DT, E5_A, E5_B, 256, 256, 2, 4><<<dim3(uint32_t(plan.groups)), 512, 0, stream>>>(
-          operand(a), operand(b), blocks, uint32_t(ceil_div(a.rows, 256)), uint32_t(ceil_div(b.rows, 256)),
-          static_cast<T*>(out.data), out.row_stride);
-  } else if (plan.tile == 128) {
-    matmul_tiles<DT, E5_A, E5_B, 128, 128, 2, 2><<<dim3(uint32_t(plan.groups)), 256, 0, stream>>>(
-        operand(a), operand(b), blocks, uint32_t(ceil_div(a.rows, 128)), uint32_t(ceil_div(b.rows, 128)),
-        static_cast<T*>(out.data), out.row_stride);
-  } else if (a.rows <= 16)
-    matmul_rows<DT, E5_A, E5_B, 1><<<dim3(uint32_t(plan.groups)), 64 * kWaves, 0, stream>>>(
-        operand(a), operand(b), blocks, n_tiles, static_cast<T*>(out.data), out.row_stride);
-  else
-    matmul_rows<DT, E5_A, E5_B, kMT><<<dim3(uint32_t(plan.groups)), 64 * kWaves, 0, stream>>>(
-        operand(a), operand(b), blocks, n_tiles, static_cast<T*>(out.data), out.row_stride);
-  return hipGetLastError();
+                     const reshard_matrix_t& out, void* workspace, hipStream_t stream) {
+  switch (plan.form) {
+    case MatmulPlan::kRows: return rows_as<DT, E5_A, E5_B, 0>(plan, a, b, out, stream);
+    case MatmulPlan::kRing16: return ring_as<DT, E5_A, E5_B, 1, 1>(plan, a, b, out, workspace, stream);
+    case MatmulPlan::kRing32: return ring_as<DT, E5_A, E5_B, 2, 1>(plan, a, b, out, workspace, stream);
+    case MatmulPlan::kRing64: return ring_as<DT, E5_A, E5_B, 4, 2>(plan, a, b, out, workspace, stream);
+    case MatmulPlan::kTiles128: return tiles_as<DT, E5_A, E5_B, 128, 2, 2>(plan, a, b, out, stream);
+    default:
+      if constexpr (DT != RESHARD_DTYPE_F32) return tiles_as<DT, E5_A, E5_B, 256, 2, 4>(plan, a, b, out, stream);
+  }
+  return hipErrorInvalidValue;
+}
+
+template <int DT, bool E5_B>
+hipError_t matmul_fused(const MatmulPlan& plan, const reshard_matrix_t& a, const reshard_matrix_t& b,
+                        const reshard_matrix_t& out, hipStream_t stream) {
+  switch (a.dtype) {
+    case RESHARD_DTYPE_F32: return rows_as<DT, false, E5_B, RESHARD_DTYPE_F32>(plan, a, b, out, stream);
+    case RESHARD_DTYPE_BF16: return rows_as<DT, false, E5_B, RESHARD_DTYPE_BF16>(plan, a, b, out, stream);
+    default: return rows_as<DT, false, E5_B, RESHARD_DTYPE_F16>(plan, a, b, out, stream);
+  }
 }
 
 template <int DT>
 hipError_t matmul_formats(const MatmulPlan& plan, const reshard_matrix_t& a, const reshard_matrix_t& b,
-                          const reshard_matrix_t& out, hipStream_t stream) {
+                          const reshard_matrix_t& out, void* workspace, hipStream_t stream) {
   const bool ea = a.dtype == RESHARD_DTYPE_FP8_E5M2, eb = b.dtype == RESHARD_DTYPE_FP8_E5M2;
-  if (ea) return eb ? matmul_as<DT, true, true>(plan, a, b, out, stream) : matmul_as<DT, true, false>(plan, a, b, out, stream);
-  return eb ? matmul_as<DT, false, true>(plan, a, b, out, stream) : matmul_as<DT, false, false>(plan, a, b, out, stream);
+  if (plan.fused)
+    return eb ? matmul_fused<DT, true>(plan, a, b, out, stream) : matmul_fused<DT, false>(plan, a, b, out, stream);
+  if (ea)
+    return eb ? matmul_as<DT, true, true>(plan, a, b, out, workspace, stream)
+              : matmul_as<DT, true, false>(plan, a, b, out, workspace, stream);
+  return eb ? matmul_as<DT, false, true>(plan, a, b, out, workspace, stream)
+            : matmul_as<DT, false, false>(plan, a, b, out, workspace, stream);
 }
+
+// The largest stride of rows that the ring and the tiles take: a tile's rows
+// within 32-bit offsets.
+constexpr int64_t kMaxTileStride = int64_t(1) << 23;
 
 }  // namespace
 
 MatmulPlan plan_matmul(const reshard_matrix_t& a, const reshard_matrix_t& b, const reshard_matrix_t& out) {
   MatmulPlan p;
-  p.groups = ceil_div(b.rows, 16) * ceil_div(a.rows, a.rows <= 16 ? 16 : 16 * kMT);
-  const int64_t stride = std::max(a.block_rows ? a.row_stride : 0, b.row_stride);
-  if (a.rows > 64 && stride <= (1 << 23)) {
-    p.tile = out.dtype != RESHARD_DTYPE_F32 && ceil_div(a.rows, 256) * ceil_div(b.rows, 256) >= 192 ? 256 : 128;
-    p.groups = ceil_div(a.rows, p.tile) * ceil_div(b.rows, p.tile);
+  const int64_t blocks = blocks_of(a.cols);
+  p.fused = !a.block_rows && blocks && a.rows <= kMaxRowsForm && a.rows * blocks * kBlock <= kFusedBytes;
+  if (!a.block_rows && !p.fused && a.rows && a.cols) {
+    p.quantized = round_up(a.rows * blocks * kBlock, 256);
+    p.quantized_scales = round_up(a.rows * blocks, 256);
   }
-  if (!a.block_rows && a.rows && a.cols) {
-    p.quantized = round_up(a.rows * blocks_of(a.cols) * kBlock, 256);
-    p.quantized_scales = a.rows * blocks_of(a.cols);
+  p.steps_per_split = uint32_t(blocks);
+  if (a.rows <= kMaxRowsForm) {
+    p.form = MatmulPlan::kRows;
+    p.groups = ceil_div(b.rows, 16);
+    p.waves = rows_waves(p.groups, blocks);
+    return p;
   }
+  p.too_wide = std::max(a.block_rows ? a.row_stride : blocks * kBlock, b.row_stride) > kMaxTileStride;
+  const auto tiles = [&](int64_t bm, int64_t bn) { return ceil_div(a.rows, bm) * ceil_div(b.rows, bn); };
+  if (out.dtype != RESHARD_DTYPE_F32 && tiles(256, 256) >= 192) {
+    p.form = MatmulPlan::kTiles256;
+    p.whole = whole_tiles(tiles(256, 256));
+    p.groups = 2 * tiles(256, 256) - p.whole;
+    return p;
+  }
+  if (tiles(128, 128) >= 256) {
+    p.form = MatmulPlan::kTiles128;
+    p.whole = p.groups = tiles(128, 128);
+    return p;
+  }
+  p.form = a.rows <= 16 ? MatmulPlan::kRing16 : a.rows <= 32 ? MatmulPlan::kRing32 : MatmulPlan::kRing64;
+  const int64_t t = tiles(a.rows <= 16 ? 16 : a.rows <= 32 ? 32 : 64, kRingCols);
+  int64_t splits = 1;
+  if (t) splits = std::max<int64_t>(1, std::min(512 / t, blocks / 4));
+  // the sums' way through memory must stay small beside the operands'
+  splits = std::max<int64_t>(1, std::min(splits, (a.rows + b.rows) * blocks * kBlock / std::max<int64_t>(1, a.rows * b.rows * 8)));
+  p.steps_per_split = uint32_t(std::max<int64_t>(1, ceil_div(blocks, splits)));
+  p.splits = int(std::max<int64_t>(1, ceil_div(blocks, p.steps_per_split)));
+  p.groups = t * p.splits;
+  if (p.splits > 1) p.parts = p.splits * a.rows * round_up(b.rows, 4) * 4;
   return p;
 }
 
 hipError_t launch_matmul(const MatmulPlan& plan, const reshard_matrix_t& a, const reshard_matrix_t& b,
                          const reshard_matrix_t& out, void* workspace, hipStream_t stream) {
   reshard_matrix_t q = a;
-  if (!a.block_rows) {
+  if (!a.block_rows && !plan.fused) {
     q.dtype = RESHARD_DTYPE_FP8_E4M3;
     q.block_rows = 1;
     q.data = workspace;
@@ -354,9 +685,9 @@ hipError_t launch_matmul(const MatmulPlan& plan, const reshard_matrix_t& a, cons
     }
   }
   switch (out.dtype) {
-    case RESHARD_DTYPE_F32: return matmul_formats<RESHARD_DTYPE_F32>(plan, q, b, out, stream);
-    case RESHARD_DTYPE_BF16: return matmul_formats<RESHARD_DTYPE_BF16>(plan, q, b, out, stream);
-    default: return matmul_formats<RESHARD_DTYPE_F16>(plan, q, b, out, stream);
+    case RESHARD_DTYPE_F32: return matmul_formats<RESHARD_DTYPE_F32>(plan, q, b, out, workspace, stream);
+    case RESHARD_DTYPE_BF16: return matmul_formats<RESHARD_DTYPE_BF16>(plan, q, b, out, workspace, stream);
+    default: return matmul_formats<RESHARD_DTYPE_F16>(plan, q, b, out, workspace, stream);
   }
 }
 

@@ -37,36 +37,6 @@ Divisor divisor(uint32_t d) {
 // Rows that one launch takes, `per_row` items each: items are counted in 31 bits.
 int64_t rows_per_launch(int64_t per_row) { return std::max<int64_t>(1, ((int64_t(1) << 31) - (1 << 20)) / per_row); }
 
-// N elements of a row from column c on as binary32, zero past `cols`.
-template <int DT, int N>
-__device__ __forceinline__ void load_up(const typename Elem<DT>::type* p, int c, int cols, float* x) {
-  typedef typename Elem<DT>::type T;
-  if (c + N <= cols) {
-    const Pack<T, N> v = load_pack<T, N>(p + c);
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = Elem<DT>::up(v.v[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = c + i < cols ? Elem<DT>::up(p[c + i]) : 0.f;
-  }
-}
-
-// The largest of 16 neighbouring lanes, in all of them.
-template <int CTRL> __device__ __forceinline__ uint32_t max_with(uint32_t v) {
-  return max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), CTRL, 0xf, 0xf, true)));
-}
-__device__ __forceinline__ uint32_t max_of_16(uint32_t v) {
-  v = max_with<0xb1>(v);      // lane ^ 1
-  v = max_with<0x4e>(v);      // lane ^ 2
-  v = max_with<0x141>(v);     // 7 - lane of 8
-  return max_with<0x140>(v);  // 15 - lane of 16
-}
-
-// Eight elements as payload bytes.
-template <bool E5M2> __device__ __forceinline__ i32x2 quantize8(const float* x, float inv) {
-  return i32x2{int(quantize4<E5M2>(x[0], x[1], x[2], x[3], inv)), int(quantize4<E5M2>(x[4], x[5], x[6], x[7], inv))};
-}
-
 // Blocks of 1 x 128: sixteen lanes a block, eight elements a lane.  Workgroups are
 // dealt to the XCDs in contiguous runs: neighbours write parts of one line of
 // scale bytes, which then meet in one L2 (4096 x 4096 bf16 10.4 -> 9.3 us).  4096 x

@@ -21,6 +21,12 @@ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 inline int64_t blocks_of(int64_t cols) { return ceil_div(cols, kBlock); }
 
+// Of n tiles that take a CU each, those whose rounds over the card are full; where
+// the rest are at most half a round, two workgroups share each of them (4096 x 14336
+// in tiles of 256 x 256 is 3.5 rounds).  Otherwise all n.
+constexpr int64_t kCus = 256;
+inline int64_t whole_tiles(int64_t n) { return n % kCus <= kCus / 2 && n > kCus ? n / kCus * kCus : n; }
+
 // Workgroups of one launch at most: a dispatch counts its work-items in 32 bits
 // (512 of them in the largest workgroup used here).
 constexpr int64_t kMaxGroups = (int64_t(1) << 23) - 1;
@@ -31,11 +37,19 @@ hipError_t launch_dequantize(const reshard_matrix_t& src, const reshard_matrix_t
 
 // How a product runs: workspace bytes and launches.
 struct MatmulPlan {
-  int tile = 0;              // rows and columns of a tile (0: the form for few rows)
+  enum Form { kRows, kRing16, kRing32, kRing64, kTiles128, kTiles256 };
+  Form form = kRows;
+  int waves = 0;             // of a workgroup (kRows)
+  bool fused = false;        // a plain a is quantized by the product's own workgroups (kRows)
+  bool too_wide = false;     // a stride that the form does not take
+  int splits = 1;            // workgroups that share a tile's contraction (kRing)
+  uint32_t steps_per_split = 0;
+  int64_t whole = 0;         // tiles of which each is one workgroup's (kTiles)
   int64_t groups = 0;        // workgroups of the product
   int64_t quantized = 0;     // bytes of a's quantized payload in the workspace (0: not needed)
   int64_t quantized_scales = 0;
-  int64_t bytes() const { return quantized + quantized_scales; }
+  int64_t parts = 0;         // bytes of the splits' sums
+  int64_t bytes() const { return quantized + quantized_scales + parts; }
 };
 MatmulPlan plan_matmul(const reshard_matrix_t& a, const reshard_matrix_t& b, const reshard_matrix_t& out);
 hipError_t launch_matmul(const MatmulPlan& plan, const reshard_matrix_t& a, const reshard_matrix_t& b,
@@ -55,6 +69,7 @@ struct GradPlan {
   int tile = 0;                  // rows and columns of a tile of dw
   int splits = 1;                // workgroups that share a tile's contraction
   uint32_t steps_per_split = 1;
+  int64_t whole = 0;             // workgroups of a whole tile, or a split of one
   int64_t groups = 0;
   bool direct = false;           // dy is read where it lies
   int64_t planes = 0;            // bytes of dy as bfloat16 planes in the workspace

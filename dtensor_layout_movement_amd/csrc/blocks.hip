@@ -166,7 +166,9 @@ reshard_status_t check_matmul(const reshard_matrix_t* a, const reshard_matrix_t*
   if (a->cols != b->cols) return report(RESHARD_ERR_INVALID_ARGUMENT, "a and b differ in columns (the contraction)");
   if (out->rows != a->rows || out->cols != b->rows)
     return report(RESHARD_ERR_INVALID_ARGUMENT, "out is not (rows of a) x (rows of b)");
-  if (rs::plan_matmul(*a, *b, *out).groups > rs::kMaxGroups) return too_many();
+  const rs::MatmulPlan p = rs::plan_matmul(*a, *b, *out);
+  if (p.too_wide) return report(RESHARD_ERR_INVALID_ARGUMENT, "rows more than 2^23 bytes apart with more than 4 rows of a");
+  if (p.groups > rs::kMaxGroups) return too_many();
   return RESHARD_OK;
 }
 

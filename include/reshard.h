@@ -591,6 +591,8 @@ reshard_status_t reshard_block_dequantize(const reshard_matrix_t* src, const res
  * 1e-5 to 8e-5 of the result's norm, well under the output's rounding); for F32
  * every product is exact.  An infinite element (E5M2) or a sum past binary32 gives an
  * infinity or a NaN, as in floating point.
+ * With more than 4 rows of a, the rows of 8-bit operands are at most 2^23 bytes
+ * apart (a plain a has at most 2^23 columns).
  * workspace: device memory of at least reshard_block_matmul_workspace bytes (0:
  * may be NULL), 16-byte aligned, not shared with a call that may run at the same
  * time.  Its contents need no preparation.

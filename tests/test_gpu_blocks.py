@@ -255,11 +255,13 @@ def test_matmul_quantizes_a_plain_operand(mnk, in_type):
         check_product(two.view, av @ bv.T, np.abs(av) @ np.abs(bv).T, k, dtype, True)
 
 
-@pytest.mark.parametrize("mnk", [(300, 24600, 300), (2100, 6000, 131), (6400, 2049, 1153), (513, 25000, 640)], ids=str)
+@pytest.mark.parametrize("mnk", [(300, 24600, 300), (2100, 6000, 131), (6400, 2049, 1153), (513, 25000, 640),
+                                 (520, 24900, 300), (65, 16500, 8400)], ids=str)
 @pytest.mark.parametrize("formats", [(E4M3, E4M3), (E5M2, E5M2)], ids=str)
 def test_matmul_of_many_tiles(mnk, formats):
-    """Enough rows and columns for the largest tiles, one, odd and even numbers
-    of steps; the 64-bit product on the GPU."""
+    """Enough rows and columns for the largest tiles, a last round of halves of
+    them, odd and even numbers of steps, more steps than the scales of a ring;
+    the 64-bit product on the GPU."""
     m, n, k = mnk
     a = quantized(values_of((m, k), "normal", m, torch.float32), 1, formats[0], extra=16)
     b = quantized(values_of((n, k), "normal", n, torch.float32), 128, formats[1], extra_scales=3)
@@ -348,9 +350,11 @@ def test_grad_of_the_weight(mnk, dy_type, dw_type):
 
 
 @pytest.mark.parametrize("dy_type,fmt", [("bf16", E4M3), ("bf16", E5M2), ("f32", E4M3)])
-@pytest.mark.parametrize("mnk", [(200, 24600, 300), (129, 2056, 6001), (64, 6000, 2100), (1000, 8200, 1500)], ids=str)
+@pytest.mark.parametrize("mnk", [(200, 24600, 300), (129, 2056, 6001), (64, 6000, 2100), (1000, 8200, 1500),
+                                 (70, 24700, 700), (193, 24700, 600)], ids=str)
 def test_grad_of_many_tiles(mnk, dy_type, fmt):
-    """Enough columns for the largest tiles; the 64-bit product on the GPU."""
+    """Enough columns for the largest tiles and a last round of halves of them;
+    the 64-bit product on the GPU."""
     m, n, k = mnk
     g = values_of((m, n), "normal", m + k, torch.float32).to(DTYPES[dy_type])
     dy = Plain(m, n, DTYPES[dy_type], value=g)
