@@ -312,6 +312,8 @@ template <int DT, int PARTS> hipError_t split_as(const reshard_matrix_t& dy, uin
 }
 
 // Adds the parts of a split contraction in order.
+constexpr int kTogether = 7;
+
 template <int DT>
 __global__ __launch_bounds__(256) void join_parts(const float* parts, int n_parts, int64_t part_stride, int cols,
                                                   uint32_t width4, int64_t items, typename Elem<DT>::type* out,
@@ -321,7 +323,15 @@ __global__ __launch_bounds__(256) void join_parts(const float* parts, int n_part
     const int64_t r = i / width4;
     const int c = int(uint32_t(i - r * width4)) * 4;
     f32x4 sum = *reinterpret_cast<const f32x4*>(parts + i * 4);
-    for (int p = 1; p < n_parts; ++p) sum += *reinterpret_cast<const f32x4*>(parts + p * part_stride + i * 4);
+    for (int p = 1; p < n_parts; p += kTogether) {  // loads of several parts under way together
+      f32x4 v[kTogether];
+#pragma unroll
+      for (int q = 0; q < kTogether; ++q)
+        v[q] = *reinterpret_cast<const f32x4*>(parts + min(p + q, n_parts - 1) * part_stride + i * 4);
+#pragma unroll
+      for (int q = 0; q < kTogether; ++q)
+        if (p + q < n_parts) sum += v[q];
+    }
     typename Elem<DT>::type* o = out + r * out_stride + c;
 #pragma unroll
     for (int e = 0; e < 4; ++e)

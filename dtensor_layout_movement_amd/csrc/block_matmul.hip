@@ -201,14 +201,15 @@ __device__ __forceinline__ Buffer rows_of(const Operand& o, int r0, int rows, ui
   return buffer_of(o.data + r0 * o.stride, uint32_t(last) * uint32_t(o.stride) + blocks * kBlock);
 }
 
-// A lane's offsets (row and chunk) in the staging of the rows from r0 on; rows
-// past the operand's last are read from the last (their results are not stored).
+// A lane's offsets (row and chunk) in the staging of an operand's rows.  Rows past
+// the operand's last lie past the buffer's end, where a load fetches nothing and
+// gives zeros (and their results are not stored).
 template <int ROWS, int THREADS>
-__device__ __forceinline__ void stage_offsets(const Operand& o, int r0, uint32_t (&off)[ROWS * 8 / THREADS]) {
+__device__ __forceinline__ void stage_offsets(const Operand& o, uint32_t (&off)[ROWS * 8 / THREADS]) {
 #pragma unroll
   for (int i = 0; i < ROWS * 8 / THREADS; ++i) {
     const int at = i * THREADS + int(threadIdx.x), row = at >> 3;
-    off[i] = uint32_t(min(row, o.rows - 1 - r0)) * uint32_t(o.stride) + uint32_t(slot_of(row, at & 7) * 16);
+    off[i] = uint32_t(row) * uint32_t(o.stride) + uint32_t(slot_of(row, at & 7) * 16);
   }
 }
 
@@ -218,12 +219,24 @@ __device__ __forceinline__ i32x8 fragment(const uint8_t* lo, const uint8_t* hi, 
   return i32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
 
-// Scale bytes of four steps of one row.
-__device__ __forceinline__ uint32_t load_scales(const uint8_t* row, uint32_t k, uint32_t blocks) {
-  if (k + 4 <= blocks) return load_pack<uint32_t, 1>(reinterpret_cast<const uint32_t*>(row + k)).v[0];
-  uint32_t v = 0;
-  for (uint32_t i = 0; k + i < blocks; ++i) v |= uint32_t(row[k + i]) << (8 * i);
-  return v;
+// Scale bytes of the steps k .. k + 3 < blocks + 3 of one row (any value past the
+// last step).  SHORT: a row of fewer than four.
+template <bool SHORT> __device__ __forceinline__ uint32_t load_scales(const uint8_t* row, uint32_t k, uint32_t blocks) {
+  if (SHORT) {
+    uint32_t v = 0;
+#pragma unroll
+    for (uint32_t i = 0; i < 3; ++i) v |= uint32_t(row[min(k + i, blocks - 1)]) << (8 * i);
+    return v;
+  }
+  const uint32_t at = min(k, blocks - 4);  // the row's last four at most
+  return load_pack<uint32_t, 1>(reinterpret_cast<const uint32_t*>(row + at)).v[0] >> (8 * (k - at));
+}
+
+// Where the scale of row r of an operand lies within a step's: (wave, lane row,
+// fragment), so that one read gives a lane those of all its wave's FRAGMENTS, which
+// the instruction selects from.
+template <int FRAGMENTS> __device__ __forceinline__ int scale_place(int r) {
+  return r / (16 * FRAGMENTS) * (16 * FRAGMENTS) + r % 16 * FRAGMENTS + r / 16 % FRAGMENTS;
 }
 
 constexpr uint32_t kBand = 8;
@@ -249,8 +262,8 @@ __device__ __forceinline__ void make_tile(const Operand& a, const Operand& b, ui
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
   uint32_t off_a[BM * 8 / kThreads], off_b[BN * 8 / kThreads];
-  stage_offsets<BM, kThreads>(a, m0, off_a);
-  stage_offsets<BN, kThreads>(b, n0, off_b);
+  stage_offsets<BM, kThreads>(a, off_a);
+  stage_offsets<BN, kThreads>(b, off_b);
   const Buffer base_a = rows_of(a, m0, BM, blocks), base_b = rows_of(b, n0, BN, blocks);
   const auto load = [&](uint8_t* to, uint32_t k) {
     stage<BM, kThreads>(base_a, off_a, k * kBlock, to, wave);
@@ -267,19 +280,12 @@ __device__ __forceinline__ void make_tile(const Operand& a, const Operand& b, ui
     else
       srow[i] = b.scales + int64_t(min(n0 + r - BM, b.rows - 1) >> b.row_shift) * b.scale_stride;
   }
-  // Within a step's scales the rows of a lane in all fragments of its wave lie
-  // together, so that one read gives a lane four of them, which the instruction
-  // selects from.
-  const auto scale_place = [](int r) {  // row r = (wave row, fragment, lane row)
-    if (r < BM) return r / (16 * kM) * (16 * kM) + r % 16 * kM + r / 16 % kM;
-    const int q = r - BM;
-    return BM + q / (16 * kN) * (16 * kN) + q % 16 * kN + q / 16 % kN;
-  };
   static_assert(kM % 4 == 0 && kN % 4 == 0, "four scales a word");
   uint32_t held_scales[kScaleRows];
   const auto load_scale_group = [&](uint32_t k) {
 #pragma unroll
-    for (int i = 0; i < kScaleRows; ++i) held_scales[i] = load_scales(srow[i], k, blocks);
+    for (int i = 0; i < kScaleRows; ++i)
+      held_scales[i] = blocks < 4 ? load_scales<true>(srow[i], k, blocks) : load_scales<false>(srow[i], k, blocks);
   };
   const auto store_scale_group = [&](uint32_t k) {
 #pragma unroll
@@ -287,7 +293,8 @@ __device__ __forceinline__ void make_tile(const Operand& a, const Operand& b, ui
       const int r = int(threadIdx.x) + i * kThreads;
       if (r < BM + BN)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) scales[((k + e) & 7) * (BM + BN) + scale_place(r)] = uint8_t(held_scales[i] >> (8 * e));
+        for (int e = 0; e < 4; ++e) scales[((k + e) & 7) * (BM + BN) + (r < BM ? scale_place<kM>(r) : BM + scale_place<kN>(r - BM))] =
+              uint8_t(held_scales[i] >> (8 * e));
     }
   };
 
@@ -460,8 +467,8 @@ __global__ __launch_bounds__(256) void matmul_ring(Operand a, Operand b, uint32_
   const uint32_t first = split * steps_per_split, last = min(first + steps_per_split, blocks);
 
   uint32_t off_a[kRowsA * 8 / kThreads], off_b[BN * 8 / kThreads];
-  stage_offsets<kRowsA, kThreads>(a, m0, off_a);
-  stage_offsets<BN, kThreads>(b, n0, off_b);
+  stage_offsets<kRowsA, kThreads>(a, off_a);
+  stage_offsets<BN, kThreads>(b, off_b);
   const Buffer base_a = rows_of(a, m0, kRowsA, blocks), base_b = rows_of(b, n0, BN, blocks);
   const auto load = [&](uint8_t* to, uint32_t k) {
     stage<kRowsA, kThreads>(base_a, off_a, k * kBlock, to, wave);
@@ -479,21 +486,48 @@ __global__ __launch_bounds__(256) void matmul_ring(Operand a, Operand b, uint32_
   const auto step = [&](const uint8_t* tile, uint32_t s) {
     const uint8_t* sk = scales + s * (kRowsA + BN);
     i32x8 x[kM], y[kN];
-    uint32_t sa[kM], sb[kN];
+    uint32_t sa = 0, sb = 0;
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
+    for (int i = 0; i < kN; ++i)
       y[i] = fragment(tile + row_b * kBlock + slot0, tile + row_b * kBlock + slot1, i * 16 * kBlock);
-      sb[i] = sk[row_b + i * 16];
-    }
-#pragma unroll
-    for (int j = 0; j < kM; ++j) {
-      x[j] = fragment(tile + row_a * kBlock + slot0, tile + row_a * kBlock + slot1, j * 16 * kBlock);
-      sa[j] = sk[row_a + j * 16];
-    }
 #pragma unroll
     for (int j = 0; j < kM; ++j)
+      x[j] = fragment(tile + row_a * kBlock + slot0, tile + row_a * kBlock + slot1, j * 16 * kBlock);
+    __builtin_memcpy(&sa, __builtin_assume_aligned(sk + wm * (16 * kM) + frow * kM, kM), kM);
+    __builtin_memcpy(&sb, __builtin_assume_aligned(sk + kRowsA + wn * (16 * kN) + frow * kN, kN), kN);
+    for_each_index<kM>([&](auto J) {
+      constexpr int j = decltype(J)::value;
+      for_each_index<kN>([&](auto I) {
+        constexpr int i = decltype(I)::value;
+        acc[i][j] = step128<kExact, E5_B, E5_A, i, j>(y[i], sb, x[j], sa, acc[i][j]);
+      });
+    });
+  };
+  // A thread's scales: kGroups words of four steps, all loaded before any is put
+  // down.  A step's are laid out as in scale_place.
+  constexpr int kGroups = (kRowsA + BN) * (kChunk / 4) / kThreads;
+  static_assert((kRowsA + BN) * (kChunk / 4) % kThreads == 0, "");
+  const auto load_chunk_scales = [&](uint32_t chunk, uint32_t steps, auto is_short) {
+    uint32_t v[kGroups];
 #pragma unroll
-      for (int i = 0; i < kN; ++i) acc[i][j] = step128<kExact, E5_B, E5_A>(y[i], sb[i], x[j], sa[j], acc[i][j]);
+    for (int n = 0; n < kGroups; ++n) {
+      const uint32_t i = threadIdx.x + n * kThreads, g = i % (kChunk / 4) * 4;
+      const int r = int(i / (kChunk / 4));
+      const uint8_t* from =
+          r < kRowsA ? a.scales + int64_t(min(m0 + r, a.rows - 1) >> a.row_shift) * a.scale_stride
+                     : b.scales + int64_t(min(n0 + r - kRowsA, b.rows - 1) >> b.row_shift) * b.scale_stride;
+      v[n] = load_scales<decltype(is_short)::value>(from, chunk + min(g, steps - 1) / 4 * 4, blocks);
+    }
+#pragma unroll
+    for (int n = 0; n < kGroups; ++n) {
+      const uint32_t i = threadIdx.x + n * kThreads, g = i % (kChunk / 4) * 4;
+      const int r = int(i / (kChunk / 4));
+      const int at = r < kRowsA ? scale_place<kM>(r) : kRowsA + scale_place<kN>(r - kRowsA);
+      if (g < steps) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) scales[(g + e) * (kRowsA + BN) + at] = uint8_t(v[n] >> (8 * e));
+      }
+    }
   };
 
   for (uint32_t chunk = first; chunk < last; chunk += kChunk) {
@@ -502,16 +536,8 @@ __global__ __launch_bounds__(256) void matmul_ring(Operand a, Operand b, uint32_
     __syncthreads();  // the last chunk's steps have been read
 #pragma unroll
     for (int i = 0; i < kRing - 1; ++i) load(ring[i], chunk + min(uint32_t(i), steps - 1));
-    for (uint32_t i = threadIdx.x; i < (kRowsA + BN) * (kChunk / 4); i += kThreads) {
-      const uint32_t r = i / (kChunk / 4), g = i % (kChunk / 4) * 4;
-      if (g >= steps) continue;
-      const uint8_t* from =
-          r < kRowsA ? a.scales + int64_t(min(m0 + int(r), a.rows - 1) >> a.row_shift) * a.scale_stride
-                     : b.scales + int64_t(min(n0 + int(r) - kRowsA, b.rows - 1) >> b.row_shift) * b.scale_stride;
-      const uint32_t v = load_scales(from, chunk + g, blocks);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) scales[(g + e) * (kRowsA + BN) + r] = uint8_t(v >> (8 * e));
-    }
+    if (blocks < 4) load_chunk_scales(chunk, steps, Index<1>{});
+    else load_chunk_scales(chunk, steps, Index<0>{});
     const uint32_t whole = steps / kRing * kRing;
     for (uint32_t s = 0; s < whole; s += kRing) {
 #pragma unroll
