@@ -79,11 +79,14 @@ __device__ __forceinline__ i32x8 load32(const uint8_t* p) {
 // takes to fill the card (rows_waves).  The weight's rows are the instruction's
 // first operand, so that a lane ends with four neighbouring columns of one row of
 // out.  With more rows the loads of a, which every workgroup makes, cost more than
-// the ring's trip through LDS.
+// the ring's trip through LDS.  One token through 14336 x 4096 takes 12.7 us, 4.6
+// TB/s of weights that no cache holds (14.0 with the launch); twice as many waves
+// took 25, four blocks ahead gained 5% on a contraction of 14336 and cost 20% on
+// 4096 x 4096, loads past the caches cost 5 to 20%.
 //
 // SRC: the type of a plain a of few elements (kFusedBytes), which each workgroup
 // quantizes for itself into LDS while its first weights are on their way; 0: a is
-// held.
+// held (then the 14336 x 4096 token takes 15.1 us and the quantization a launch more).
 constexpr int64_t kMaxRowsForm = 4;
 constexpr int kFusedBytes = 16384;  // payload bytes in LDS
 constexpr int kFusedPad = 16;       // between rows there: rows start in distinct banks
@@ -93,7 +96,7 @@ template <int DT, bool E5_A, bool E5_B, int SRC>
 __global__ __launch_bounds__(64 * kMaxWaves) void matmul_rows(Operand a, Operand b, int cols, uint32_t blocks,
                                                               typename Elem<DT>::type* out, int64_t out_stride) {
   constexpr bool kExact = DT == RESHARD_DTYPE_F32;
-  constexpr int kAhead = 4;
+  constexpr int kAhead = 2;
   extern __shared__ __align__(16) uint8_t lds[];  // sums of all waves, then a's payload and scales
   f32x4* sums = reinterpret_cast<f32x4*>(lds);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -181,8 +184,15 @@ int rows_waves(int64_t groups, int64_t blocks) {
 // WM x WN waves; a step takes 128 columns of both operands through LDS, loaded
 // straight there (16 bytes a lane) one step ahead into the other of two
 // buffers.  Rows lie 128 bytes apart in LDS, and 16-byte chunk c of row r sits in
-// slot c ^ (r / 2 % 8), so that the 16 rows a matrix instruction's operand
-// takes its chunk from lie in distinct banks.  A load to LDS writes lane
+// slot c ^ (r / 2 % 8); a lane's two chunks are four apart, which together puts the
+// reads of a fragment into distinct banks (no conflicts counted).
+//
+// 256 x 256 tiles: 8192^3 takes 463 us (2370 TFLOP/s), 4096 x 4096 x 14336 190 (2500),
+// 4096 x 14336 x 4096 256 to 280 (1720 to 1880; 32 steps a tile leave more of it to
+// filling and writing).  Bound by power first: with operands of zeros the same
+// kernel runs at 2800.  Then by the matrix pipe waiting at the step's barrier; a wave
+// tile of 128 x 128, which reads less from LDS, made the compiler move sums
+// between register files and took 450 us.  A load to LDS writes lane
 // order, so the permutation is made on the address that each lane loads.
 __device__ __forceinline__ int slot_of(int row, int chunk) { return chunk ^ ((row >> 1) & 7); }
 
@@ -432,11 +442,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tiles(Operand a, Opera
 
 // The ring form, for products that do not fill the card with large tiles: a
 // workgroup of four waves makes a BM x 64 tile over the steps [first, last) of the
-// contraction.  Such products are bound by the latency of their loads, so four LDS
-// buffers keep three steps under way; a step waits for the oldest only.  The
-// scales of up to kChunk steps are put into LDS beforehand.  Where the tiles are
-// few, several workgroups share a contraction and write binary32 sums that
-// join_parts adds in order.
+// contraction.  Such products are bound by the latency of their loads (without
+// them 300 x 4096 x 14336 would take 34 of its 51 us with warm weights), so four
+// LDS buffers keep three steps under way; a step waits for the oldest only.  The
+// scales of up to kChunk steps are put into LDS beforehand, all loaded together
+// (one after another they cost 7 of those 51 us).  Where the tiles are few, several
+// workgroups share a contraction and write binary32 sums that join_parts adds in
+// order.  33 x 4096 x 14336 takes 19.8 us (the form for few rows 31), 301 x 5000 x
+// 3001 fp16 14 to 17 (128 x 128 tiles 20).
 constexpr int kRing = 4, kChunk = 64, kRingCols = 64;
 
 // Waits for all but `left` of this wave's loads to LDS and for its LDS reads, then
@@ -685,7 +698,10 @@ MatmulPlan plan_matmul(const reshard_matrix_t& a, const reshard_matrix_t& b, con
   p.form = a.rows <= 16 ? MatmulPlan::kRing16 : a.rows <= 32 ? MatmulPlan::kRing32 : MatmulPlan::kRing64;
   const int64_t t = tiles(a.rows <= 16 ? 16 : a.rows <= 32 ? 32 : 64, kRingCols);
   int64_t splits = 1;
-  if (t) splits = std::max<int64_t>(1, std::min(512 / t, blocks / 4));
+  // Two workgroups a CU at once.  From a tile a CU on a contraction is only worth
+  // sharing when long: 300 x 4096 x 14336 62 -> 53 us in three parts, but 128 x 14336
+  // x 4096 27 -> 35 in two.
+  if (t) splits = std::max<int64_t>(1, t < kCus ? std::min(2 * kCus / t, blocks / 4) : std::min(4 * kCus / t, blocks / 32));
   // the sums' way through memory must stay small beside the operands'
   splits = std::max<int64_t>(1, std::min(splits, (a.rows + b.rows) * blocks * kBlock / std::max<int64_t>(1, a.rows * b.rows * 8)));
   p.steps_per_split = uint32_t(std::max<int64_t>(1, ceil_div(blocks, splits)));
