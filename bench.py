@@ -34,7 +34,9 @@ The two-stage transport of the pages (each destination box delivered once,
 split over its replicas, then assembled by every replica; pipelined over
 tensor chunks on two streams) is timed the same way as ``two_stage_gpu``, and
 the pages' hybrid refit (FFN projections by the reshard, other weights by
-gather-then-slice) as ``hybrid_gpu`` where the workload has both kinds.
+gather-then-slice) as ``hybrid_gpu`` where the workload has both kinds.  The
+refit of the same weights to 8-bit blocks (quantized, then moved as payload and
+scales) is ``quantized_refit_gpu`` where the layouts do not cut blocks.
 
 ``cpu_baseline`` times the oracle (the pages' gather-then-slice scheme, run on
 the host) on the same input bytes the GPU consumed and checks that its output
@@ -323,6 +325,47 @@ def hybrid(torch, wl, sets_boxes, stream, steps: int, reshard_ms: float):
                 "reshard_speedup": round(ms / reshard_ms, 3)}
     finally:
         hp.close()
+
+
+def quantized(torch, R, wl, lay_src, lay_dst, sets, stream, steps: int, reshard_ms: float):
+    """The refit of the same weights to 8 bits with a scale for each 128 x 128 block
+    (quantized.QuantizedPlan): every source shard quantized, then payload and
+    scales moved by the reshard.  None when the workload's layouts cut blocks or
+    hold tensors that are not 2-d floats."""
+    from dtensor_layout_movement_amd.quantized import QuantizedPlan
+    try:
+        qp = QuantizedPlan(wl.tensors)
+    except ValueError:
+        return None
+    try:
+        n_t = len(wl.tensors)
+        room = {(side, what): [[torch.empty(max(1, r * c), dtype=torch.uint8, device="cuda")
+                                for r, c in getattr(qp, what + "_shapes")(t, side)] for t in range(n_t)]
+                for side in ("src", "dst") for what in ("payload", "scale")}
+        ptr = {key: [[b.data_ptr() for b in per] for per in v] for key, v in room.items()}
+        bound = []
+        for src_bufs, _, _, _ in sets:
+            src = [[b.data_ptr() if b is not None else 0 for b in src_bufs[s0:s1]]
+                   for (s0, s1), _ in tensor_slices(R, lay_src, lay_dst)]
+            bound.append(qp.bind(src, ptr["src", "payload"], ptr["src", "scale"], ptr["dst", "payload"],
+                                 ptr["dst", "scale"]))
+        for i in range(3):
+            qp.execute(bound[i % len(bound)], stream.cuda_stream)
+        torch.cuda.synchronize()
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record(stream)
+        for i in range(steps):
+            qp.execute(bound[i % len(bound)], stream.cuda_stream)
+        e1.record(stream)
+        torch.cuda.synchronize()
+        ms = e0.elapsed_time(e1) / steps
+        moved = R.reshard_plan_stats(qp.plan)
+        return {"ms_per_step": round(ms, 5), "steps": steps, "bytes_moved": qp.bytes_moved(),
+                "gbps": round(qp.bytes_moved() / ms / 1e6, 1),
+                "reshard_bytes_moved": moved["bytes_read"] + moved["bytes_written"],
+                "reshard_speedup": round(ms / reshard_ms, 3)}
+    finally:
+        qp.close()
 
 
 def cpu_info() -> dict:
@@ -616,7 +659,7 @@ def main() -> int:
 
     copy_ref = torch_copy_reference(torch, dev, stream, algo_bytes, args.min_footprint_gb)
 
-    reference = comparator = two = mixed = None
+    reference = comparator = two = mixed = eight = None
     if not args.no_comparator:
         print("[bench] comparators", file=sys.stderr, flush=True)
         reference = contiguous_reference(torch, R, st, dev, stream, max(5, K // 4), args.min_footprint_gb)
@@ -632,6 +675,7 @@ def main() -> int:
             per_tensor.append((sp, dp))
         two = two_stage(torch, wl, per_tensor, max(5, K // 4), ms_per_step)
         mixed = hybrid(torch, wl, per_tensor, stream, max(5, K // 4), ms_per_step)
+        eight = quantized(torch, R, wl, lay_src, lay_dst, sets, stream, max(5, K // 4), ms_per_step)
         torch.cuda.empty_cache()
     plan_us = plan_timing(R, wl, args.plan_reps if algo_bytes < 2e10 else max(5, args.plan_reps // 20))
     spec0 = wl.tensors[0]
@@ -683,6 +727,7 @@ def main() -> int:
         "gather_then_slice_gpu": comparator,
         "two_stage_gpu": two,
         "hybrid_gpu": mixed,
+        "quantized_refit_gpu": eight,
         "wall_s": head["wall_s"],
     }
     if not args.no_cpu_baseline:

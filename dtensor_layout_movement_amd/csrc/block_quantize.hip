@@ -34,8 +34,11 @@ Divisor divisor(uint32_t d) {
   magic_u31(d, &v.m, &v.s);
   return v;
 }
-// Rows that one launch takes, `per_row` items each: items are counted in 31 bits.
-int64_t rows_per_launch(int64_t per_row) { return std::max<int64_t>(1, ((int64_t(1) << 31) - (1 << 20)) / per_row); }
+// Rows that one launch takes, `per_row` items each of which a workgroup takes
+// `per_group`: items are counted in 31 bits and workgroups to kMaxGroups.
+int64_t rows_per_launch(int64_t per_row, int64_t per_group) {
+  return std::max<int64_t>(1, std::min((int64_t(1) << 31) - (1 << 20), kMaxGroups * per_group) / per_row);
+}
 
 // Blocks of 1 x 128: sixteen lanes a block, eight elements a lane.  Workgroups are
 // dealt to the XCDs in contiguous runs: neighbours write parts of one line of
@@ -153,8 +156,9 @@ __global__ __launch_bounds__(kThreads) void quantize_squares(const typename Elem
 constexpr int kBack = 2;
 
 template <int DT, bool E5M2>
-__global__ __launch_bounds__(kThreads) void dequantize_rows(Held src, int row_shift, Divisor chunks, uint32_t items,
-                                                            typename Elem<DT>::type* dst, int64_t stride, int cols) {
+__global__ __launch_bounds__(kThreads) void dequantize_rows(Held src, int64_t first_row, int row_shift, Divisor chunks,
+                                                            uint32_t items, typename Elem<DT>::type* dst,
+                                                            int64_t stride, int cols) {
   typedef typename Elem<DT>::type T;
   constexpr int N = 16 / sizeof(T);
   const uint32_t first = blockIdx.x * (kThreads * kBack) + threadIdx.x;
@@ -169,7 +173,7 @@ __global__ __launch_bounds__(kThreads) void dequantize_rows(Held src, int row_sh
     const Pack<uint32_t, N / 4> v = load_pack<uint32_t, N / 4>(p);
 #pragma unroll
     for (int k = 0; k < N / 4; ++k) q[u][k] = v.v[k];
-    s[u] = src.scales[int64_t(row[u] >> row_shift) * src.scale_stride + c[u] / kBlock];
+    s[u] = src.scales[((first_row + row[u]) >> row_shift) * src.scale_stride + c[u] / kBlock];
   }
 #pragma unroll
   for (int u = 0; u < kBack; ++u) {
@@ -201,7 +205,7 @@ hipError_t quantize_as(const reshard_matrix_t& src, const reshard_matrix_t& dst,
   const uint32_t blocks = uint32_t(blocks_of(src.cols));
   if (dst.block_rows == 1) {
     const Held to = held(dst);
-    const int64_t rows = rows_per_launch(blocks);
+    const int64_t rows = rows_per_launch(blocks, kThreads / 16);
     for (int64_t r = 0; r < src.rows; r += rows) {
       const uint32_t items = uint32_t(std::min(rows, src.rows - r) * blocks);
       quantize_rows<DT, E5M2><<<dim3(uint32_t(ceil_div(items, kThreads / 16))), kThreads, 0, stream>>>(
@@ -228,14 +232,12 @@ hipError_t dequantize_as(const reshard_matrix_t& src, const reshard_matrix_t& ds
   constexpr int N = 16 / sizeof(T);
   const uint32_t chunks = uint32_t(ceil_div(src.cols, N));
   const Held from = held(src);
-  int64_t rows = rows_per_launch(chunks);
-  if (rows < src.rows) rows = std::max<int64_t>(rows / kBlock, 1) * kBlock;  // whole blocks
+  const int64_t rows = rows_per_launch(chunks, kThreads * kBack);
   for (int64_t r = 0; r < src.rows; r += rows) {
     const uint32_t items = uint32_t(std::min(rows, src.rows - r) * chunks);
     dequantize_rows<DT, E5M2><<<dim3(uint32_t(ceil_div(items, kThreads * kBack))), kThreads, 0, stream>>>(
-        Held{from.data + r * from.stride, from.stride, from.scales + r / src.block_rows * from.scale_stride,
-             from.scale_stride},
-        src.block_rows == 1 ? 0 : 7, divisor(chunks), items, static_cast<T*>(dst.data) + r * dst.row_stride,
+        Held{from.data + r * from.stride, from.stride, from.scales, from.scale_stride}, r, src.block_rows == 1 ? 0 : 7,
+        divisor(chunks), items, static_cast<T*>(dst.data) + r * dst.row_stride,
         dst.row_stride, int(dst.cols));
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

@@ -52,20 +52,31 @@ reshard_status_t check_shape(const reshard_matrix_t* m, const char* name, Kind k
                                    : "dtype is not F32, BF16, F16, FP8_E4M3 or FP8_E5M2");
 }
 
-// The bytes a matrix spans.
+// The bytes a matrix spans: rows of `width` bytes, `stride` apart.
 struct Span {
   uintptr_t lo, hi;
+  uintptr_t width, stride;
 };
 Span data_span(const reshard_matrix_t& m) {
-  const int64_t cols = m.block_rows ? rs::blocks_of(m.cols) * rs::kBlock : m.cols;
+  const int64_t cols = m.block_rows ? rs::blocks_of(m.cols) * rs::kBlock : m.cols, size = elem_size(m.dtype);
   const uintptr_t lo = reinterpret_cast<uintptr_t>(m.data);
-  return Span{lo, lo + uintptr_t(((m.rows - 1) * m.row_stride + cols) * elem_size(m.dtype))};
+  return Span{lo, lo + uintptr_t(((m.rows - 1) * m.row_stride + cols) * size), uintptr_t(cols * size),
+              uintptr_t(m.row_stride * size)};
 }
 Span scale_span(const reshard_matrix_t& m) {
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(m.scales);
-  return Span{lo, lo + uintptr_t((rs::ceil_div(m.rows, m.block_rows) - 1) * m.scale_stride + rs::blocks_of(m.cols))};
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(m.scales), width = uintptr_t(rs::blocks_of(m.cols));
+  return Span{lo, lo + uintptr_t((rs::ceil_div(m.rows, m.block_rows) - 1) * m.scale_stride) + width, width,
+              uintptr_t(m.scale_stride)};
 }
-bool overlap(const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi; }
+// Whether two matrices share bytes.  Rows of one stride may lie between each
+// other's (columns of one larger matrix); with different strides whole spans count.
+bool overlap(const Span& a, const Span& b) {
+  if (a.lo >= b.hi || b.lo >= a.hi) return false;
+  if (a.stride != b.stride || !a.stride) return true;
+  if (b.lo < a.lo) return overlap(b, a);
+  const uintptr_t d = (b.lo - a.lo) % a.stride;
+  return d < a.width || d + b.width > a.stride;
+}
 
 // Pointers and alignment of one matrix with elements (host only).
 reshard_status_t check_pointers(const reshard_matrix_t& m, const char* name) {
@@ -108,7 +119,7 @@ reshard_status_t check_call(std::initializer_list<Use> uses, const void* workspa
   for (const Use& u : uses)
     if (!empty(*u.m))
       if (const reshard_status_t s = check_pointers(*u.m, u.name)) return s;
-  Span work{0, 0};
+  Span work{};
   if (given < need)
     return report(RESHARD_ERR_INVALID_ARGUMENT, "workspace of " + std::to_string(given) + " bytes, " +
                                                     std::to_string(need) + " needed");
@@ -120,13 +131,13 @@ reshard_status_t check_call(std::initializer_list<Use> uses, const void* workspa
   }
   for (const Use& w : uses) {
     if (empty(*w.m)) continue;
-    const Span wd = data_span(*w.m), ws = w.m->block_rows ? scale_span(*w.m) : Span{0, 0};
+    const Span wd = data_span(*w.m), ws = w.m->block_rows ? scale_span(*w.m) : Span{};
     if (need && (overlap(wd, work) || overlap(ws, work))) return bad(w.name, "overlaps the workspace");
     if (!w.written) continue;
     if (w.m->block_rows && overlap(wd, ws)) return bad(w.name, "scales overlap the data");
     for (const Use& r : uses) {
       if (&r == &w || empty(*r.m)) continue;
-      const Span rd = data_span(*r.m), rsc = r.m->block_rows ? scale_span(*r.m) : Span{0, 0};
+      const Span rd = data_span(*r.m), rsc = r.m->block_rows ? scale_span(*r.m) : Span{};
       if (overlap(wd, rd) || overlap(wd, rsc) || overlap(ws, rd) || overlap(ws, rsc))
         return report(RESHARD_ERR_INVALID_ARGUMENT, std::string(w.name) + " overlaps " + r.name);
     }

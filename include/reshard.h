@@ -540,7 +540,7 @@ void reshard_plan_destroy(reshard_plan_t plan);
  * device; NULL = default stream), allocate nothing, hold no state between calls
  * and may be captured into a HIP graph (each is one to three kernel launches).
  * Pointers are borrowed as in reshard_execute; a matrix that is written must
- * not overlap another one of the call.  Matrices with no elements are allowed
+ * not overlap another one of the call (columns of one larger matrix are fine).  Matrices with no elements are allowed
  * (pointers and strides are not looked at).  Results do not depend on timing: no atomics, every sum
  * in a fixed order.  Errors, checked before anything is launched:
  * RESHARD_ERR_INVALID_ARGUMENT (shape, type, stride, alignment, overlap, host
@@ -589,7 +589,8 @@ reshard_status_t reshard_block_dequantize(const reshard_matrix_t* src, const res
  * F16 the products go through the 8-bit matrix instructions, which drop the low
  * bits of small products beside large ones within one instruction (measured
  * 1e-5 to 8e-5 of the result's norm, well under the output's rounding); for F32
- * every product is exact.  An infinite element (E5M2) or a sum past binary32 gives an
+ * every product is exact (elements below 2^-126, where bfloat16 has fewer bits, may
+ * be rounded or lost).  An infinite element (E5M2) or a sum past binary32 gives an
  * infinity or a NaN, as in floating point.
  * With more than 4 rows of a, the rows of 8-bit operands are at most 2^23 bytes
  * apart (a plain a has at most 2^23 columns).

@@ -111,6 +111,21 @@ def test_matmul_same_handle_twice_is_refused_as_an_overlap():
     refused(BAD, "overlap", R.reshard_block_matmul, x, held(130, 130, 128), x, 8 * P, 1 << 20)
 
 
+def test_columns_of_one_larger_matrix_do_not_overlap():
+    """a in the left, out in the right columns of rows of 512 elements: accepted as
+    far as the device; one element more of either is not."""
+    w = held(128, 256, 128, data=5 * P, scales=6 * P)
+    room = (8 * P, 1 << 20)
+    left = R.matrix(40, 256, H, P, 512)
+    for out, ok in ((R.matrix(40, 128, H, P + 512, 512), True), (R.matrix(40, 128, H, P + 768, 512), True),
+                    (R.matrix(40, 128, H, P + 510, 512), False), (R.matrix(40, 128, H, P + 770, 512), False),
+                    (R.matrix(40, 128, H, P - 256, 512), True), (R.matrix(40, 128, H, P - 254, 512), False)):
+        if not ok:
+            refused(BAD, "out overlaps a", R.reshard_block_matmul, left, w, out, *room)
+        elif not torch.cuda.is_available():
+            refused(R.ERR_HIP, "hipGetDevice", R.reshard_block_matmul, left, w, out, *room)
+
+
 @pytest.mark.parametrize("dy,x,dw,status,text", [
     (held(5, 9, data=5 * P), held(5, 130), plain(9, 130, **OUT), BAD, "dy: dtype"),
     (plain(5, 9), plain(5, 130), plain(9, 130, **OUT), BAD, "x: dtype"),

@@ -550,6 +550,32 @@ def test_offsets_past_32_bits():
     src.check_rest()
 
 
+def test_more_blocks_than_one_launch_takes():
+    """Quantizing past 2^27 blocks and reading back past 2^31 pieces: rows on both
+    sides of the launches' borders."""
+    rows, cols = (1 << 27) + 4096, 128
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("needs 100 GB of device memory")
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    payload = torch.full((rows, cols), CANARY, dtype=torch.uint8, device="cuda")
+    scales = torch.full((rows, 1), CANARY, dtype=torch.uint8, device="cuda")
+    marks = [0, (1 << 27) - (1 << 16) - 20, (1 << 27) - 36, (1 << 27) + 10, rows - 40]
+    for i, at in enumerate(marks):  # in order: a later one may overwrite rows of an earlier one
+        x[at:at + 40] = values_of((40, cols), "normal", i, torch.bfloat16).cuda()
+    h = R.matrix(rows, cols, E4M3, payload.data_ptr(), cols, 1, scales.data_ptr(), 1)
+    xm = R.matrix(rows, cols, R.DTYPE_BF16, x.data_ptr(), cols)
+    R.reshard_block_quantize(xm, h, None, stream())
+    torch.cuda.synchronize()
+    wants = {at: ref.quantize(x[at:at + 40], 1)[0] for at in marks}
+    assert int((scales == CANARY).sum()) == 0
+    x.fill_(7.0)
+    R.reshard_block_dequantize(h, xm, stream())
+    torch.cuda.synchronize()
+    for at in marks:
+        assert np.array_equal(x[at:at + 40].double().cpu().numpy(), wants[at]), at
+    assert sum(int((part[:, 0] == 7.0).sum()) for part in x.split(1 << 24)) == 0  # nothing was left as it was
+
+
 def test_results_do_not_change_from_call_to_call():
     m, n, k = 130, 515, 2000
     a = quantized(values_of((m, k), "normal", 1, torch.float32), 1)
