@@ -349,6 +349,7 @@ __device__ __forceinline__ void make_tile(const Operand& a, const Operand& b, ui
       return fragment(tile + row_a * kBlock + slot0, tile + row_a * kBlock + slot1, j * 16 * kBlock);
     };
     i32x8 next = fragment_a(1);
+    __builtin_amdgcn_s_setprio(1);  // before waves that copy and multiply up: 261 us for 266 at 4096x14336x4096
     for_each_index<kM - 2>([&](auto J) {
       const i32x8 second = fragment_a(decltype(J)::value + 2);
       products(J, y, sb, x, sa);
@@ -364,6 +365,7 @@ __device__ __forceinline__ void make_tile(const Operand& a, const Operand& b, ui
     for (int i = 0; i < kN / 4; ++i) sbl[i] = sb[i];
 #pragma unroll
     for (int j = 0; j < kM / 4; ++j) sal[j] = sa[j];
+    __builtin_amdgcn_s_setprio(0);
     turn();
     products(Index<kM - 2>{}, yl, sbl, xl, sal);
     products(Index<kM - 1>{}, yl, sbl, next, sal);
@@ -378,21 +380,23 @@ __device__ __forceinline__ void make_tile(const Operand& a, const Operand& b, ui
     begin(tile0, 0);
   }
   // The next four steps' scales are loaded in one step and put down in the next,
-  // into the group that was last read four steps ago.
+  // into the group that was last read four steps ago.  A turn asks for the
+  // block after next before it reads the next one's first fragments: 8192^3 takes
+  // 464 us for 469 the other way round.
   for (uint32_t k = 0; k + 1 < blocks; k += 2) {
     const bool scale_turn = (k & 2) == 0 && k + 4 < blocks, more = k + 2 < blocks;
     if (scale_turn) load_scale_group(k + 4);
     step(tile0, [&] {
       __syncthreads();  // tile1 has arrived, tile0 has been read
-      begin(tile1, k + 1);
       if (more) load(tile0, k + 2);
+      begin(tile1, k + 1);
       if (scale_turn) store_scale_group(k + 4);
     });
     step(tile1, [&] {
       __syncthreads();
       if (more) {
-        begin(tile0, k + 2);
         if (k + 3 < blocks) load(tile1, k + 3);
+        begin(tile0, k + 2);
       }
     });
   }
