@@ -686,7 +686,7 @@ MatmulPlan plan_matmul(const reshard_matrix_t& a, const reshard_matrix_t& b, con
     p.waves = rows_waves(p.groups, blocks);
     return p;
   }
-  p.too_wide = std::max(a.block_rows ? a.row_stride : blocks * kBlock, b.row_stride) > kMaxTileStride;
+  p.too_wide = blocks && b.rows && std::max(a.block_rows ? a.row_stride : blocks * kBlock, b.row_stride) > kMaxTileStride;
   const auto tiles = [&](int64_t bm, int64_t bn) { return ceil_div(a.rows, bm) * ceil_div(b.rows, bn); };
   if (out.dtype != RESHARD_DTYPE_F32 && tiles(256, 256) >= 192) {
     p.form = MatmulPlan::kTiles256;

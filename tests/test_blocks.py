@@ -149,6 +149,17 @@ def test_workspace_queries_check_shapes_and_need_no_pointers():
     refused(BAD, "dw is not", R.reshard_block_grad_workspace, o, q, R.matrix(71, 300, F, 0))
 
 
+def test_strides_of_matrices_without_elements_mean_nothing():
+    # no contraction: a and b have no elements, and rows any distance apart
+    a, b = R.matrix(70, 0, E, None, 1 << 40, 1, None, -5), R.matrix(9, 0, E, None, 1 << 24, 128, None, 0)
+    assert R.reshard_block_matmul_workspace(a, b, plain(70, 9)) == 0
+    # no columns of out: b has no elements
+    b = R.matrix(0, 130, E, None, 1 << 24, 128, None, 0)
+    assert R.reshard_block_matmul_workspace(held(70, 130), b, R.matrix(70, 0, H, None, -1)) == 0
+    # with elements on both sides the limit holds
+    refused(BAD, "2^23", R.reshard_block_matmul_workspace, held(70, 130), held(9, 130, 128, stride=1 << 24), plain(70, 9))
+
+
 def test_valid_calls_fail_cleanly_without_a_gpu():
     if torch.cuda.is_available():
         pytest.skip("a GPU is visible")
