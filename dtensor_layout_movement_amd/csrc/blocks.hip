@@ -106,7 +106,7 @@ reshard_status_t check_memory(const void* p, const char* name, int dev) {
     (void)hipGetLastError();  // not an error of any launch
     return e == hipErrorInvalidValue ? bad(name, "not device memory") : hip_fail(e, "hipPointerGetAttributes");
   }
-  if (at.type == hipMemoryTypeUnregistered) return bad(name, "not device memory");
+  if (at.type == hipMemoryTypeUnregistered || at.type == hipMemoryTypeHost) return bad(name, "not device memory");
   if (at.type == hipMemoryTypeDevice && at.device != dev)
     return report(RESHARD_ERR_DEVICE_MISMATCH, std::string(name) + " is on device " + std::to_string(at.device) +
                                                    ", current device is " + std::to_string(dev));

@@ -539,14 +539,15 @@ void reshard_plan_destroy(reshard_plan_t plan);
  * All calls here are asynchronous on `stream` (a hipStream_t of the current
  * device; NULL = default stream), allocate nothing, hold no state between calls
  * and may be captured into a HIP graph (each is one to three kernel launches).
- * Pointers are borrowed as in reshard_execute; a matrix that is written must
- * not overlap another one of the call (columns of one larger matrix are fine).  Matrices with no elements are allowed
- * (pointers and strides are not looked at).  Results do not depend on timing: no atomics, every sum
- * in a fixed order.  Errors, checked before anything is launched:
- * RESHARD_ERR_INVALID_ARGUMENT (shape, type, stride, alignment, overlap, host
- * memory, workspace too small), RESHARD_ERR_NULL_SHARD (NULL data or scales of a
- * matrix with elements), RESHARD_ERR_DEVICE_MISMATCH (a matrix or the stream on
- * another device than the current one), RESHARD_ERR_HIP.
+ * Pointers are borrowed as in reshard_execute; a matrix that is written must not
+ * overlap another one of the call (columns of one larger matrix are fine).
+ * Matrices with no elements are allowed (their pointers and strides are not looked
+ * at).  Results do not depend on timing: no atomics, every sum in a fixed order.
+ * Errors, checked before anything is launched: RESHARD_ERR_INVALID_ARGUMENT
+ * (shape, type, stride, alignment, overlap, host memory, pinned or not, workspace
+ * too small), RESHARD_ERR_NULL_SHARD (NULL data or scales of a matrix with
+ * elements), RESHARD_ERR_DEVICE_MISMATCH (a matrix or the stream on another device
+ * than the current one), RESHARD_ERR_HIP.
  */
 #define RESHARD_BLOCK 128
 

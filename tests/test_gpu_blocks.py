@@ -465,6 +465,18 @@ def test_host_memory_is_refused():
     assert bool((h.payload == CANARY).all())
 
 
+def test_pinned_host_memory_is_refused():
+    x = torch.ones(4, 128, dtype=torch.bfloat16, pin_memory=True)
+    h, back = Held(4, 128, 1), R.matrix(4, 128, R.DTYPE_BF16, x.data_ptr())
+    for call, name in ((lambda: R.reshard_block_quantize(back, h.m, None, stream()), "src"),
+                       (lambda: R.reshard_block_dequantize(h.m, back, stream()), "dst")):
+        with pytest.raises(R.ReshardError) as e:
+            call()
+        assert e.value.status == R.ERR_INVALID_ARGUMENT and name in str(e.value)
+    torch.cuda.synchronize()
+    assert bool((h.payload == CANARY).all()) and bool((x == 1).all())
+
+
 def test_another_stream_and_two_calls_at_once():
     """Two products on two streams with workspaces of their own."""
     m, n, k = 200, 300, 515
