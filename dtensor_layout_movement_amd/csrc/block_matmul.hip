@@ -182,18 +182,19 @@ int rows_waves(int64_t groups, int64_t blocks) {
 
 // The tiled form.  A workgroup makes a BM (rows of a) x BN (rows of b) tile with
 // WM x WN waves; a step takes 128 columns of both operands through LDS, loaded
-// straight there (16 bytes a lane) one step ahead into the other of two
+// straight there (16 bytes a lane) during the step before into the other of two
 // buffers.  Rows lie 128 bytes apart in LDS, and 16-byte chunk c of row r sits in
 // slot c ^ (r / 2 % 8); a lane's two chunks are four apart, which together puts the
 // reads of a fragment into distinct banks (no conflicts counted).
 //
-// 256 x 256 tiles: 8192^3 takes 463 us (2370 TFLOP/s), 4096 x 4096 x 14336 190 (2500),
-// 4096 x 14336 x 4096 256 to 280 (1720 to 1880; 32 steps a tile leave more of it to
-// filling and writing).  Bound by power first: with operands of zeros the same
-// kernel runs at 2800.  Then by the matrix pipe waiting at the step's barrier; a wave
-// tile of 128 x 128, which reads less from LDS, made the compiler move sums
-// between register files and took 450 us.  A load to LDS writes lane
-// order, so the permutation is made on the address that each lane loads.
+// 256 x 256 tiles: 8192^3 takes 442 us (2490 TFLOP/s), 4096 x 4096 x 14336 180 (2670),
+// 4096 x 14336 x 4096 251 to 275 (1750 to 1920; 32 steps a tile leave more of it to
+// filling and writing).  Bound by LDS, whose reads and copies (at 128 bytes a cycle)
+// take as long as a step's products, so that every wait at the step's barrier shows,
+// and by power: operands of zeros run 20% faster.  Four waves of 128 x 128, which
+// read a third less from LDS, leave one wave a SIMD and nothing to run while it
+// waits: 473 us.  A load to LDS writes lane order, so the permutation is made on
+// the address that each lane loads.
 __device__ __forceinline__ int slot_of(int row, int chunk) { return chunk ^ ((row >> 1) & 7); }
 
 // Moves a tile's rows, 128 bytes from column byte `col` of each, into `to`.
@@ -330,10 +331,13 @@ __device__ __forceinline__ void make_tile(const Operand& a, const Operand& b, ui
     __builtin_memcpy(sa, __builtin_assume_aligned(sk + wm * (16 * kM) + frow * kM, kM), kM);
     __builtin_memcpy(sb, __builtin_assume_aligned(sk + BM + wn * (16 * kN) + frow * kN, kN), kN);
   };
-  // Step k, then what `turn` does between the step's last LDS read and its last
-  // products: those hide the barrier and the next step's first reads.  One
-  // fragment of a is read ahead of its products; the pins keep the compiler from
-  // reading all of them first, which does not fit the registers.
+  // Step k.  `fill` asks for the next step's block, behind the step's first reads:
+  // asked for in the turn, a step earlier, the copies into LDS stand in the way of
+  // the reads that all waves make there (8192^3 takes 447 us for 465, 4096 x 4096 x
+  // 14336 181 for 190).  `turn` comes between the step's last LDS read and its last
+  // products: those hide the barrier and the next step's first reads.  Two
+  // fragments of a are read ahead of their products; the pins keep the compiler
+  // from reading all of them first, which does not fit the registers.
   const auto products = [&](auto J, const i32x8 (&yj)[kN], const uint32_t (&sbj)[kN / 4], const i32x8& xj,
                             const uint32_t (&saj)[kM / 4]) {
     constexpr int j = decltype(J)::value;
@@ -344,14 +348,15 @@ __device__ __forceinline__ void make_tile(const Operand& a, const Operand& b, ui
     });
     __builtin_amdgcn_sched_barrier(0);
   };
-  const auto step = [&](const uint8_t* tile, auto turn) {
+  const auto step = [&](const uint8_t* tile, auto fill, auto turn) {
     const auto fragment_a = [&](int j) {
       return fragment(tile + row_a * kBlock + slot0, tile + row_a * kBlock + slot1, j * 16 * kBlock);
     };
     i32x8 next = fragment_a(1);
-    __builtin_amdgcn_s_setprio(1);  // before waves that copy and multiply up: 261 us for 266 at 4096x14336x4096
+    __builtin_amdgcn_s_setprio(1);  // before waves that copy: 4096 x 14336 x 4096 266 -> 261 us
     for_each_index<kM - 2>([&](auto J) {
       const i32x8 second = fragment_a(decltype(J)::value + 2);
+      if constexpr (decltype(J)::value == 0) fill();
       products(J, y, sb, x, sa);
       x = next;
       next = second;
@@ -376,31 +381,24 @@ __device__ __forceinline__ void make_tile(const Operand& a, const Operand& b, ui
     load_scale_group(0);
     store_scale_group(0);
     __syncthreads();
-    if (blocks > 1) load(tile1, 1);
     begin(tile0, 0);
   }
   // The next four steps' scales are loaded in one step and put down in the next,
-  // into the group that was last read four steps ago.  A turn asks for the
-  // block after next before it reads the next one's first fragments: 8192^3 takes
-  // 464 us for 469 the other way round.
+  // into the group that was last read four steps ago.
   for (uint32_t k = 0; k + 1 < blocks; k += 2) {
     const bool scale_turn = (k & 2) == 0 && k + 4 < blocks, more = k + 2 < blocks;
     if (scale_turn) load_scale_group(k + 4);
-    step(tile0, [&] {
+    step(tile0, [&] { load(tile1, k + 1); }, [&] {
       __syncthreads();  // tile1 has arrived, tile0 has been read
-      if (more) load(tile0, k + 2);
       begin(tile1, k + 1);
       if (scale_turn) store_scale_group(k + 4);
     });
-    step(tile1, [&] {
+    step(tile1, [&] { if (more) load(tile0, k + 2); }, [&] {
       __syncthreads();
-      if (more) {
-        if (k + 3 < blocks) load(tile1, k + 3);
-        begin(tile0, k + 2);
-      }
+      if (more) begin(tile0, k + 2);
     });
   }
-  if (blocks & 1) step(tile0, [] {});
+  if (blocks & 1) step(tile0, [] {}, [] {});
 #pragma unroll
   for (int j = 0; j < kM; ++j) {
     const int m = m0 + wm * (BM / WM) + j * 16 + frow;
