@@ -45,6 +45,20 @@ __device__ __forceinline__ void load_to_lds(Buffer from, uint8_t* to, uint32_t l
                                            int(off), 0, 0);
 }
 
+// Waits for all but `left` of this wave's loads (to LDS too) and for its LDS accesses,
+// then for the other waves: what they loaded is there, what they read may be written.
+// __syncthreads does not say this of loads to LDS: the compiler adds the wait where it
+// follows them to the barrier, but not, for one, around a loop that loads under a
+// condition.
+template <int LEFT> __device__ __forceinline__ void loads_barrier() {
+#ifdef __HIP_DEVICE_COMPILE__
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((LEFT & 15) | ((LEFT >> 4) << 14) | (7 << 4));
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+#endif
+}
+
 // Element types by their dtype code.
 template <int DT> struct Elem;
 template <> struct Elem<RESHARD_DTYPE_F32> {

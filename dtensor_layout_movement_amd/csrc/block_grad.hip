@@ -212,12 +212,12 @@ __device__ __forceinline__ void make_tile(const Output& dy, const Checkpoint& x,
     put_x(tile0, first);
   }
   for (uint32_t s = first; s + 1 < last; s += 2) {
-    __syncthreads();  // tile0 is whole, tile1 is free
+    loads_barrier<0>();  // tile0 is whole, tile1 is free
     load_x(s + 1);
     load_y(tile1, s + 1);
     step(tile0);
     put_x(tile1, s + 1);
-    __syncthreads();
+    loads_barrier<0>();
     const bool more = s + 2 < last;
     if (more) {
       load_x(s + 2);
@@ -227,7 +227,7 @@ __device__ __forceinline__ void make_tile(const Output& dy, const Checkpoint& x,
     if (more) put_x(tile0, s + 2);
   }
   if (first < last && ((last - first) & 1)) {
-    __syncthreads();
+    loads_barrier<0>();
     step(tile0);
   }
 

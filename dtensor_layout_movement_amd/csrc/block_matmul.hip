@@ -380,7 +380,7 @@ __device__ __forceinline__ void make_tile(const Operand& a, const Operand& b, ui
     load(tile0, 0);
     load_scale_group(0);
     store_scale_group(0);
-    __syncthreads();
+    loads_barrier<0>();
     begin(tile0, 0);
   }
   // The next four steps' scales are loaded in one step and put down in the next,
@@ -389,12 +389,12 @@ __device__ __forceinline__ void make_tile(const Operand& a, const Operand& b, ui
     const bool scale_turn = (k & 2) == 0 && k + 4 < blocks, more = k + 2 < blocks;
     if (scale_turn) load_scale_group(k + 4);
     step(tile0, [&] { load(tile1, k + 1); }, [&] {
-      __syncthreads();  // tile1 has arrived, tile0 has been read
+      loads_barrier<0>();  // tile1 has arrived, tile0 has been read
       begin(tile1, k + 1);
       if (scale_turn) store_scale_group(k + 4);
     });
     step(tile1, [&] { if (more) load(tile0, k + 2); }, [&] {
-      __syncthreads();
+      loads_barrier<0>();
       if (more) begin(tile0, k + 2);
     });
   }
@@ -453,15 +453,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_tiles(Operand a, Opera
 // order.  33 x 4096 x 14336 takes 19.8 us (the form for few rows 31), 301 x 5000 x
 // 3001 fp16 14 to 17 (128 x 128 tiles 20).
 constexpr int kRing = 4, kChunk = 64, kRingCols = 64;
-
-// Waits for all but `left` of this wave's loads to LDS and for its LDS reads, then
-// for the other waves.
-template <int LEFT> __device__ __forceinline__ void ring_barrier() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt((LEFT & 15) | ((LEFT >> 4) << 14) | (7 << 4));
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
 
 template <int DT, bool E5_A, bool E5_B, int MT, int WM, int OUT>
 __global__ __launch_bounds__(256) void matmul_ring(Operand a, Operand b, uint32_t blocks, uint32_t steps_per_split,
@@ -548,7 +539,7 @@ __global__ __launch_bounds__(256) void matmul_ring(Operand a, Operand b, uint32_
   for (uint32_t chunk = first; chunk < last; chunk += kChunk) {
     const uint32_t steps = min(uint32_t(kChunk), last - chunk);
     uint8_t* const ring[kRing] = {ring0, ring1, ring2, ring3};
-    __syncthreads();  // the last chunk's steps have been read
+    loads_barrier<0>();  // the last chunk's steps have been read
 #pragma unroll
     for (int i = 0; i < kRing - 1; ++i) load(ring[i], chunk + min(uint32_t(i), steps - 1));
     if (blocks < 4) load_chunk_scales(chunk, steps, Index<1>{});
@@ -560,12 +551,12 @@ __global__ __launch_bounds__(256) void matmul_ring(Operand a, Operand b, uint32_
         // step s + i has arrived for every wave, and every wave is done with the
         // step before it, whose buffer the next load takes; past the last step the
         // loads go on (to no use), so that their count stays the same
-        ring_barrier<(kRing - 2) * kLoads>();
+        loads_barrier<(kRing - 2) * kLoads>();
         load(ring[(i + kRing - 1) % kRing], chunk + min(s + i + kRing - 1, steps - 1));
         step(ring[i], s + i);
       }
     }
-    ring_barrier<0>();  // the last three steps have arrived; no load may outlive its use of LDS
+    loads_barrier<0>();  // the last three steps have arrived; no load may outlive its use of LDS
 #pragma unroll
     for (int i = 0; i < kRing - 1; ++i)
       if (whole + i < steps) step(ring[i], whole + i);
