@@ -34,6 +34,7 @@ def gpu():
     torch.cuda.set_device(0)
     yield
     torch.cuda.synchronize()
+    torch.cuda.empty_cache()
 
 
 def up(a, b):
@@ -403,3 +404,44 @@ def test_gradients_with_scales_at_their_ends(m, n, k, dy_type, fmt):
     tol = m * planes * (2.0 ** -24 * mass + torch.where(torch.arange(k, device="cuda") < 128, 2.0 ** -126, 0.0))
     fine = ~torch.isnan(want)
     assert bool(((got - want).abs() <= tol + 2.0 ** -24 * want.abs())[fine].all())
+
+
+# ------------------------------------------------- rows as far apart as they may be
+
+
+def room_for(gib):
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < gib << 30:
+        pytest.skip(f"needs {gib} GB of device memory")
+
+
+def spread_out(rows, cols, block_rows, seed, stride, **kw):
+    return filled(rows, cols, block_rows, E4M3, seed, extra=stride - up(cols, BLOCK) * BLOCK, **kw)
+
+
+@pytest.mark.parametrize("out_type", ["bf16", "f32"])
+@pytest.mark.parametrize("m,n,k,stride", [(3, 70, 300, 1 << 28), (20, 300, 300, 1 << 23), (300, 260, 300, 1 << 23),
+                                          (2100, 4100, 300, 1 << 23), (2100, 6000, 300, 1 << 23)])
+def test_products_of_rows_far_apart(m, n, k, stride, out_type):
+    """More than 2^31 bytes from a tile's first row to its last, 2^23 between rows
+    (any distance with few rows)."""
+    room_for(100)
+    a, b = spread_out(m, k, 1, 1, stride), spread_out(n, k, 128, 2, stride)
+    out = Plain(m, n, DTYPES[out_type])
+    matmul(a.m, b.m, out)
+    check_product(a, b, out)
+
+
+@pytest.mark.parametrize("stride", [1 << 24, (1 << 24) + 8])
+@pytest.mark.parametrize("m,n,k", [(70, 200, 300), (129, 6000, 2100)])
+def test_gradients_of_rows_far_apart(m, n, k, stride):
+    """dy's rows 2^25 bytes apart, where they are read in place, and a little more;
+    x's 2^26."""
+    room_for(60)
+    g = torch.Generator(device="cuda").manual_seed(m)
+    v = torch.randn(m, n, generator=g, device="cuda").bfloat16()
+    dy, x = Plain(m, n, torch.bfloat16, stride=stride, value=v), spread_out(m, k, 1, 4, 1 << 26)
+    dw = Plain(n, k, torch.float32)
+    grad(dy, x.m, dw)
+    gv, xv = v.double().t().contiguous(), decoded(x)
+    within(dw.view, gv @ xv, m * 2.0 ** -24 * (gv.abs() @ xv.abs()), torch.float32)
