@@ -160,6 +160,27 @@ def test_strides_of_matrices_without_elements_mean_nothing():
     refused(BAD, "2^23", R.reshard_block_matmul_workspace, held(70, 130), held(9, 130, 128, stride=1 << 24), plain(70, 9))
 
 
+@pytest.mark.parametrize("rows,ok", [((1 << 27) - 16, True), ((1 << 27) - 15, False), (1 << 30, False)])
+def test_products_of_more_workgroups_than_one_launch_takes_are_refused(rows, ok):
+    """2^23 - 1 at most, with few rows one for each 16 columns of out."""
+    w, out = held(rows, 100, 128), R.matrix(1, rows, H, P)
+    if ok:
+        assert R.reshard_block_matmul_workspace(plain(1, 100), w, out) == 0
+    else:
+        refused(BAD, "too many tiles", R.reshard_block_matmul_workspace, plain(1, 100), w, out)
+        refused(BAD, "too many tiles", R.reshard_block_matmul, plain(1, 100), w, out)
+
+
+@pytest.mark.parametrize("rows,ok", [((1 << 27) - 128, True), ((1 << 27) - 127, False), (1 << 30, False)])
+def test_weights_of_more_blocks_than_one_launch_takes_are_refused(rows, ok):
+    """2^23 - 1 blocks of 128 x 128 at most, here eight for each 128 rows."""
+    src, dst = plain(rows, 1024), held(rows, 1024, 128, data=1 << 45, scales=1 << 50)
+    if not ok:
+        refused(BAD, "too many tiles", R.reshard_block_quantize, src, dst)
+    elif not torch.cuda.is_available():
+        refused(R.ERR_HIP, "hipGetDevice", R.reshard_block_quantize, src, dst)
+
+
 def test_valid_calls_fail_cleanly_without_a_gpu():
     if torch.cuda.is_available():
         pytest.skip("a GPU is visible")
