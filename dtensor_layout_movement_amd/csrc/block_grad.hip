@@ -83,7 +83,8 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 // LDS holds a step's rows one after another; the 32-byte pieces (16 columns) of a
 // row are permuted by the row, so that the eight rows that half a wave turns at
-// a time lie in distinct banks.
+// a time lie in distinct banks.  (The stores of the widened x, 32 bytes a lane in two
+// halves, meet two to a bank: a fifth of the LDS cycles of a large gradient.)
 __device__ __forceinline__ int piece_of(int row, int piece) { return piece ^ ((row & 3) | ((row >> 1) & 4)); }
 
 // A lane's four values down the rows of one column: lanes 4 e .. 4 e + 3 of each 16
@@ -104,7 +105,12 @@ __device__ __forceinline__ bf16x8 fragment(const uint8_t* p, int half) {
 // WN x WK waves over the steps [first, last) of the contraction, within the
 // caller's LDS, two buffers of kDepth * (BN + BK) * 2 bytes.  The next step's dy goes
 // straight to LDS and its x to registers while this step is multiplied; x is then
-// widened and put into the other buffer.
+// widened and put into the other buffer.  dw of 14336 x 4096 over 4096 rows of bf16
+// takes 499 us (960 TFLOP/s, the matrix pipe busy 43% of the time; a bfloat16 library
+// product 505): the waits at a step's barrier, with two waves a SIMD.  Short ones pay
+// each step's latency, one being under way: 1024 x 4096 over 257 rows (128 x 128 tiles, 5
+// steps) 10.8 us.  An fp32 dy goes over x three times: 5000 x 3001 over 301 rows 44 us
+// and 6.8 for the planes, an fp16 one twice: 4096 x 4096 over 1024 rows 79 and 7.
 template <int DT_W, bool E5M2, int BN, int BK, int WN, int WK>
 __device__ __forceinline__ void make_tile(const Output& dy, const Checkpoint& x, int rows, int n0, int k0,
                                           uint32_t first, uint32_t last, typename Elem<DT_W>::type* base,
@@ -369,6 +375,9 @@ hipError_t launch_join(const float* parts, int n_parts, int64_t part_stride, con
 GradPlan plan_grad(const reshard_matrix_t& dy, const reshard_matrix_t& x, const reshard_matrix_t& dw) {
   GradPlan p;
   const int64_t rows = dy.rows * grad_planes(dy.dtype), steps = ceil_div(rows, kDepth);
+  // Large tiles where they nearly fill the card, us against 128 x 128: dw of 4096 x 4096
+  // (256 of them) over 4096 rows 132 to 141 and 169, 14336 x 4096 over 257 69 and 85, 5000 x
+  // 3001 (240) over 301 of fp32 48 and 56; 4096 x 2048 (128) over 4096 128 and 85 to 91.
   p.tile = ceil_div(dy.cols, 256) * ceil_div(x.cols, 256) >= 192 ? 256 : 128;
   const int64_t tiles = ceil_div(dy.cols, p.tile) * ceil_div(x.cols, p.tile);
   // Few tiles and a long contraction: several workgroups share it.

@@ -69,8 +69,9 @@ __global__ __launch_bounds__(kThreads) void quantize_rows(const typename Elem<DT
 // rows, turns them four by four with byte permutes and stores 16 bytes of four
 // rows of the transpose; eight lanes make a whole 128-byte row of it.  Rows lie 33
 // dwords apart and the lower half 8 dwords further, which puts the 64 dwords of a
-// read into distinct banks.  14336 x 4096 fp32 takes 53 us, 66 with the transpose
-// (5.6 and 5.3 TB/s); gathering the transpose byte by byte took 75.
+// read into distinct banks.  14336 x 4096 fp32 takes 53 us, 65 with the transpose
+// (5.6 and 5.4 TB/s), bf16 40 (4.4); 5000 x 3001 bf16 13 and 16.7 us (3.4 and 3.6 TB/s).
+// Gathering the transpose byte by byte took 75 for 66.
 __device__ __forceinline__ int lds_row(int r) { return r * 33 + (r >> 6) * 8; }
 
 template <int DT, bool E5M2, bool TRANSPOSE>
@@ -151,7 +152,7 @@ __global__ __launch_bounds__(kThreads) void quantize_squares(const typename Elem
 // Reading back: as many elements a lane as make 16 bytes of output, so that a
 // wave's stores are contiguous, kBack pieces a lane whose loads are under way
 // together, stores past the caches (kept in them, 4096 x 14336 bf16 took 32 us
-// instead of 25.8, 6.8 TB/s with the payload still in the last-level cache; 16
+// instead of 26, 6.8 TB/s with the payload still in the last-level cache; 16
 // elements a lane whatever the type took 50).
 constexpr int kBack = 2;
 
