@@ -342,6 +342,54 @@ def test_a_scale_that_is_not_a_number(m, n, k, out_type, fmt):
     assert bool(torch.isfinite(out.view.float())[~want].all())
 
 
+@pytest.mark.parametrize("out_type", list(DTYPES))
+@pytest.mark.parametrize("m,n,k", EACH)
+def test_infinite_elements_stay_in_their_row_and_column(m, n, k, out_type):
+    """E5M2 payloads may hold infinities (quantizing writes none)."""
+    a, b = filled(m, k, 1, E5M2, 7, spread=0), filled(n, k, 128, E5M2, 8, spread=0)
+    for h in (a, b):
+        h.scales[:h.srows, :h.blocks] -= 10  # results within fp16's range
+    a.payload[1, k - 1], b.payload[n - 1, 3] = 0x7c, 0xfc
+    out = Plain(m, n, DTYPES[out_type])
+    matmul(a.m, b.m, out)
+    want = torch.zeros(m, n, dtype=torch.bool, device="cuda")
+    want[1], want[:, n - 1] = True, True
+    assert torch.equal(~torch.isfinite(out.view.float()), want)
+
+
+@pytest.mark.parametrize("m,n,k", [(4, 300, 8000), (8, 300, 8000), (300, 260, 2000), (2100, 4100, 300), (2100, 6000, 300)])
+def test_large_forms_captured_and_replayed(m, n, k):
+    """A projection and its weight gradient of every form in one graph, replayed with
+    other inputs and eager work in between: the eager calls' bytes."""
+    x, dy = Plain(m, k, torch.bfloat16), Plain(m, n, torch.bfloat16)
+    q, b = Held(m, k, 1), filled(n, k, 128, E4M3, n)
+    outs = [Plain(m, n, torch.bfloat16), Plain(n, k, torch.bfloat16)]
+    need = max(R.reshard_block_matmul_workspace(x.m, b.m, outs[0].m), R.reshard_block_grad_workspace(dy.m, q.m, outs[1].m))
+    room = torch.empty(max(1, need), dtype=torch.uint8, device="cuda")
+
+    def step():
+        R.reshard_block_quantize(x.m, q.m, None, stream())
+        R.reshard_block_matmul(x.m, b.m, outs[0].m, room.data_ptr(), need, stream())
+        R.reshard_block_grad(dy.m, q.m, outs[1].m, False, room.data_ptr(), need, stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for seed in range(4):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        x.view.copy_(torch.randn(m, k, generator=g, device="cuda"))
+        dy.view.copy_(torch.randn(m, n, generator=g, device="cuda"))
+        step()
+        torch.cuda.synchronize()
+        eager = [o.view.clone() for o in outs]
+        for o in outs:
+            o.view.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        for o, e in zip(outs, eager):
+            assert same_bytes(o.view, e)
+            o.check_rest()
+
+
 # ------------------------------------------------------------- gradients
 
 GRADS = [(64, 130, 260, "128"), (1, 300, 500, "128"), (700, 200, 300, "128"), (3000, 2100, 200, "128"), (130, 4100, 1100, "128"),
