@@ -10,6 +10,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 REPO_DIR = os.path.dirname(PKG_DIR)
@@ -37,9 +39,22 @@ def hipcc() -> str:
 
 
 def build(verbose: bool = False) -> str:
-    """Compile SOURCES into libreshard.so; return its path."""
-    tmp = LIB_PATH + ".tmp"
-    cmd = [hipcc(), *HIP_FLAGS, "-shared", "-I", INCLUDE, "-I", CSRC, *SOURCES, "-o", tmp]
+    """Compile SOURCES, each on its own and several at a time, and link them into
+    libreshard.so; return its path."""
+    with tempfile.TemporaryDirectory() as folder:
+        jobs = []
+        for src in SOURCES:
+            obj = os.path.join(folder, os.path.basename(src) + ".o")
+            jobs.append(([hipcc(), *HIP_FLAGS, "-c", "-I", INCLUDE, "-I", CSRC, src, "-o", obj], obj))
+        with ThreadPoolExecutor(min(8, int(os.environ.get("MAX_JOBS", 8)))) as pool:
+            list(pool.map(lambda job: _run(job[0], verbose), jobs))
+        tmp = LIB_PATH + ".tmp"
+        _run([hipcc(), *HIP_FLAGS, "-shared", *[obj for _, obj in jobs], "-o", tmp], verbose)
+    os.replace(tmp, LIB_PATH)
+    return LIB_PATH
+
+
+def _run(cmd, verbose) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -50,8 +65,6 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError("hipcc failed:\n" + "\n".join(msgs))
     if verbose and msgs:
         print("\n".join(msgs), flush=True)
-    os.replace(tmp, LIB_PATH)
-    return LIB_PATH
 
 
 if __name__ == "__main__":
