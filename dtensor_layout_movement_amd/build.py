@@ -18,8 +18,10 @@ REPO_DIR = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(REPO_DIR, "include")
 LIB_PATH = os.path.join(PKG_DIR, "libreshard.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("plan.cpp", "kernel.hip", "reshard.hip", "blocks.hip",
-                                           "block_quantize.hip", "block_matmul.hip", "block_grad.hip")]
+SOURCES = [os.path.join(CSRC, f) for f in ("plan.cpp", "kernel.hip", "reshard.hip", "checks.cpp",
+                                           "blocks.hip", "block_quantize.hip", "block_matmul.hip", "block_grad.hip",
+                                           "groups.hip", "group_quantize.hip", "group_matmul.hip",
+                                           "expert_route.hip")]
 
 # Packed-fp32 instructions are kept out of every HIP object; the copy kernel does
 # no floating point and the block-scaled products do theirs on the matrix cores,

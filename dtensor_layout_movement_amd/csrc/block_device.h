@@ -6,6 +6,7 @@
 
 #include <cstdint>
 
+#include "plan.h"
 #include "reshard.h"
 
 namespace rs {
@@ -22,6 +23,17 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 __device__ __forceinline__ uint32_t run_of(uint32_t id, uint32_t n) {
   const uint32_t xcd = id % 8;
   return xcd * (n / 8) + min(xcd, n % 8) + id / 8;
+}
+
+// n / d for n < 2^31 by a multiplier (magic_u31 of plan.h).
+struct Divisor {
+  uint32_t d, m, s;
+};
+__device__ __forceinline__ uint32_t quotient(uint32_t n, const Divisor& v) { return (__umulhi(n, v.m) + n) >> v.s; }
+inline Divisor divisor(uint32_t d) {
+  Divisor v{d, 0, 0};
+  magic_u31(d, &v.m, &v.s);
+  return v;
 }
 
 // Keeps a value in registers at this point of the program: no use of it moves

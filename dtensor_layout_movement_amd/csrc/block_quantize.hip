@@ -3,7 +3,6 @@
 // written once.
 #include "block_device.h"
 #include "blocks.h"
-#include "plan.h"
 
 #include <algorithm>
 
@@ -22,22 +21,6 @@ struct Held {
 
 Held held(const reshard_matrix_t& m) {
   return Held{static_cast<uint8_t*>(m.data), m.row_stride, static_cast<uint8_t*>(m.scales), m.scale_stride};
-}
-
-// n / d for n < 2^31 by a multiplier (magic_u31 of plan.h).
-struct Divisor {
-  uint32_t d, m, s;
-};
-__device__ __forceinline__ uint32_t quotient(uint32_t n, const Divisor& v) { return (__umulhi(n, v.m) + n) >> v.s; }
-Divisor divisor(uint32_t d) {
-  Divisor v{d, 0, 0};
-  magic_u31(d, &v.m, &v.s);
-  return v;
-}
-// Rows that one launch takes, `per_row` items each of which a workgroup takes
-// `per_group`: items are counted in 31 bits and workgroups to kMaxGroups.
-int64_t rows_per_launch(int64_t per_row, int64_t per_group) {
-  return std::max<int64_t>(1, std::min((int64_t(1) << 31) - (1 << 20), kMaxGroups * per_group) / per_row);
 }
 
 // Blocks of 1 x 128: sixteen lanes a block, eight elements a lane.  Workgroups are

@@ -5,15 +5,12 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
-#include <string>
 
 #include "reshard.h"
 
 namespace rs {
-
-// Keeps `msg` as the calling thread's last error and returns `s` (reshard.hip).
-reshard_status_t report(reshard_status_t s, const std::string& msg);
 
 constexpr int kBlock = RESHARD_BLOCK;
 
@@ -31,6 +28,12 @@ inline int64_t whole_tiles(int64_t n) { return n % kCus <= kCus / 2 && n > kCus 
 // Workgroups of one launch at most: a dispatch counts its work-items in 32 bits
 // (512 of them in the largest workgroup used here).
 constexpr int64_t kMaxGroups = (int64_t(1) << 23) - 1;
+
+// Rows that one launch takes, `per_row` items each of which a workgroup takes
+// `per_group`: items are counted in 31 bits and workgroups to kMaxGroups.
+inline int64_t rows_per_launch(int64_t per_row, int64_t per_group) {
+  return std::max<int64_t>(1, std::min((int64_t(1) << 31) - (1 << 20), kMaxGroups * per_group) / per_row);
+}
 
 hipError_t launch_quantize(const reshard_matrix_t& src, const reshard_matrix_t& dst, const reshard_matrix_t* dst_t,
                            hipStream_t stream);

@@ -10,7 +10,7 @@
 #include <string>
 #include <vector>
 
-#include "blocks.h"
+#include "checks.h"
 #include "kernel.h"
 #include "plan.h"
 #include "reshard.h"

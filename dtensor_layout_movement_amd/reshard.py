@@ -35,6 +35,7 @@ DTYPE_U8, DTYPE_I8, DTYPE_BOOL, DTYPE_FP8_E4M3, DTYPE_FP8_E5M2 = 0, 1, 2, 3, 4
 DTYPE_BF16, DTYPE_F16, DTYPE_I16 = 5, 6, 7
 DTYPE_F32, DTYPE_I32 = 8, 9
 DTYPE_F64, DTYPE_I64 = 10, 11
+DTYPE_FP4_E2M1 = 12  # two to a byte: group-scaled matrices only
 
 DESC_ITEMS = 0       # rows of items of `unit` bytes
 DESC_DST_CHUNKS = 1  # rows cut into destination-aligned 16-byte chunks
@@ -60,6 +61,9 @@ EXPORTED = (
     "reshard_plan_descriptors", "reshard_plan_segments", "reshard_plan_destroy",
     "reshard_block_quantize", "reshard_block_dequantize", "reshard_block_matmul",
     "reshard_block_matmul_workspace", "reshard_block_grad", "reshard_block_grad_workspace",
+    "reshard_group_quantize", "reshard_group_dequantize", "reshard_group_matmul", "reshard_group_matmul_workspace",
+    "reshard_expert_sort", "reshard_expert_sort_workspace", "reshard_expert_gather", "reshard_expert_combine",
+    "reshard_expert_combine_grad", "reshard_expert_matmul", "reshard_expert_matmul_workspace",
     "reshard_last_error",
 )
 
@@ -106,6 +110,9 @@ class Segment(ctypes.Structure):
 assert ctypes.sizeof(Segment) == 32
 
 BLOCK = 128  # columns of a scale block
+GROUP = 32  # columns of a scale group
+MAX_EXPERTS = 1024
+MAX_CHOICES = 64
 
 
 class Matrix(ctypes.Structure):
@@ -170,6 +177,17 @@ def _load() -> ctypes.CDLL:
         "reshard_block_matmul_workspace": (st, [_MATP, _MATP, _MATP, _I64P]),
         "reshard_block_grad": (st, [_MATP, _MATP, _MATP, ctypes.c_int, _VP, _I64, _VP]),
         "reshard_block_grad_workspace": (st, [_MATP, _MATP, _MATP, _I64P]),
+        "reshard_group_quantize": (st, [_MATP, _MATP, _VP]),
+        "reshard_group_dequantize": (st, [_MATP, _MATP, _VP]),
+        "reshard_group_matmul": (st, [_MATP, _MATP, _MATP, _VP, _I64, _VP]),
+        "reshard_group_matmul_workspace": (st, [_MATP, _MATP, _MATP, _I64P]),
+        "reshard_expert_sort": (st, [_VP, ctypes.c_int, _I64, ctypes.c_int, _I64, _I64, _VP, _VP, _VP, _I64, _VP]),
+        "reshard_expert_sort_workspace": (st, [_I64, ctypes.c_int, _I64, _I64P]),
+        "reshard_expert_gather": (st, [_MATP, _VP, ctypes.c_int, _MATP, _VP]),
+        "reshard_expert_combine": (st, [_MATP, _VP, ctypes.c_int, _MATP, _MATP, _VP]),
+        "reshard_expert_combine_grad": (st, [_MATP, _MATP, _VP, ctypes.c_int, _MATP, _MATP, _MATP, _VP]),
+        "reshard_expert_matmul": (st, [_MATP, _MATP, _VP, _I64, _MATP, _VP, _I64, _VP]),
+        "reshard_expert_matmul_workspace": (st, [_MATP, _MATP, _I64, _MATP, _I64P]),
         "reshard_last_error": (ctypes.c_char_p, []),
     }
     for name, (res, args) in sig.items():
@@ -417,13 +435,15 @@ def reshard_plan_destroy(plan: int) -> None:
 
 def matrix(rows: int, cols: int, dtype: int, data: int | None, row_stride: int | None = None, block_rows: int = 0,
            scales: int | None = None, scale_stride: int | None = None) -> Matrix:
-    """Describe a matrix in device memory for the block-scaled calls (reusable
-    across calls; the memory stays the caller's).  ``block_rows`` 0: a plain
-    F32, BF16 or F16 matrix; 1 or 128: an FP8 payload with ``scales``.  Strides
-    default to the smallest that the format allows."""
-    blocks = -(-int(cols) // BLOCK)
+    """Describe a matrix in device memory for the block-scaled, group-scaled and
+    experts' calls (reusable across calls; the memory stays the caller's).
+    ``block_rows`` 0: a plain F32, BF16 or F16 matrix; 1 or 128: an FP8 payload
+    with ``scales``; 1 with ``DTYPE_FP4_E2M1``: a 4-bit payload, ``row_stride`` in
+    elements.  Strides default to the smallest that the format allows."""
+    block = GROUP if dtype == DTYPE_FP4_E2M1 else BLOCK
+    blocks = -(-int(cols) // block)
     if row_stride is None:
-        row_stride = blocks * BLOCK if block_rows else cols
+        row_stride = blocks * block if block_rows else cols
     if scale_stride is None:
         scale_stride = blocks if block_rows else 0
     return Matrix(int(rows), int(cols), int(dtype), int(block_rows), data or None, int(row_stride), scales or None,
@@ -464,6 +484,80 @@ def reshard_block_grad(dy: Matrix, x: Matrix, dw: Matrix, accumulate: bool = Fal
     """dw[n, k] (+)= sum of dy[m, n] * x[m, k] from the 8-bit checkpoint ``x``."""
     _check(_load().reshard_block_grad(dy, x, dw, int(bool(accumulate)), workspace or None, int(workspace_bytes),
                                       stream or None))
+
+
+def reshard_group_quantize(src: Matrix, dst: Matrix, stream: int | None = None) -> None:
+    """Quantize ``src`` into the group-scaled 4-bit ``dst``."""
+    _check(_load().reshard_group_quantize(src, dst, stream or None))
+
+
+def reshard_group_dequantize(src: Matrix, dst: Matrix, stream: int | None = None) -> None:
+    _check(_load().reshard_group_dequantize(src, dst, stream or None))
+
+
+def reshard_group_matmul_workspace(a: Matrix, b: Matrix, out: Matrix) -> int:
+    """Bytes of device workspace that reshard_group_matmul needs."""
+    n = ctypes.c_int64()
+    _check(_load().reshard_group_matmul_workspace(a, b, out, ctypes.byref(n)))
+    return n.value
+
+
+def reshard_group_matmul(a: Matrix, b: Matrix, out: Matrix, workspace: int | None = None, workspace_bytes: int = 0,
+                         stream: int | None = None) -> None:
+    """out[m, n] = sum of a[m, k] * b[n, k], ``b`` a group-scaled 4-bit weight."""
+    _check(_load().reshard_group_matmul(a, b, out, workspace or None, int(workspace_bytes), stream or None))
+
+
+def reshard_expert_sort_workspace(tokens: int, choices: int, experts: int) -> int:
+    """Bytes of device workspace that reshard_expert_sort needs."""
+    n = ctypes.c_int64()
+    _check(_load().reshard_expert_sort_workspace(int(tokens), int(choices), int(experts), ctypes.byref(n)))
+    return n.value
+
+
+def reshard_expert_sort(ids: int | None, ids_dtype: int, tokens: int, choices: int, first: int, experts: int,
+                        offsets: int | None, position: int | None, workspace: int | None = None,
+                        workspace_bytes: int = 0, stream: int | None = None) -> None:
+    """Rows of the choices ``ids`` (address, DTYPE_I32 or DTYPE_I64) of the experts
+    ``first`` to ``first + experts - 1``: each expert's ``offsets`` and each choice's
+    ``position`` (addresses of int32 arrays)."""
+    _check(_load().reshard_expert_sort(ids or None, int(ids_dtype), int(tokens), int(choices), int(first), int(experts),
+                                       offsets or None, position or None, workspace or None, int(workspace_bytes),
+                                       stream or None))
+
+
+def reshard_expert_gather(x: Matrix, position: int | None, choices: int, rows: Matrix,
+                          stream: int | None = None) -> None:
+    """rows[position[t, j]] = x[t]."""
+    _check(_load().reshard_expert_gather(x, position or None, int(choices), rows, stream or None))
+
+
+def reshard_expert_combine(rows: Matrix, position: int | None, choices: int, weights: Matrix | None, out: Matrix,
+                           stream: int | None = None) -> None:
+    """out[t] = sum of weights[t, j] * rows[position[t, j]]; ``weights`` None: of 1."""
+    _check(_load().reshard_expert_combine(rows, position or None, int(choices), weights, out, stream or None))
+
+
+def reshard_expert_combine_grad(dout: Matrix, rows: Matrix | None, position: int | None, choices: int,
+                                weights: Matrix | None, drows: Matrix | None, dweights: Matrix | None,
+                                stream: int | None = None) -> None:
+    """Gradients of reshard_expert_combine: of its rows and of its weights (either may be None)."""
+    _check(_load().reshard_expert_combine_grad(dout, rows, position or None, int(choices), weights, drows, dweights,
+                                               stream or None))
+
+
+def reshard_expert_matmul_workspace(a: Matrix, b: Matrix, experts: int, out: Matrix) -> int:
+    """Bytes of device workspace that reshard_expert_matmul needs."""
+    n = ctypes.c_int64()
+    _check(_load().reshard_expert_matmul_workspace(a, b, int(experts), out, ctypes.byref(n)))
+    return n.value
+
+
+def reshard_expert_matmul(a: Matrix, b: Matrix, offsets: int | None, experts: int, out: Matrix,
+                          workspace: int | None = None, workspace_bytes: int = 0, stream: int | None = None) -> None:
+    """Rows ``offsets[e]`` to ``offsets[e + 1] - 1`` of ``a`` times expert e's weight, row by row of ``out``."""
+    _check(_load().reshard_expert_matmul(a, b, offsets or None, int(experts), out, workspace or None,
+                                         int(workspace_bytes), stream or None))
 
 
 def reshard_last_error() -> str:

@@ -100,6 +100,7 @@ typedef enum reshard_dtype {
   RESHARD_DTYPE_I32 = 9,
   RESHARD_DTYPE_F64 = 10,
   RESHARD_DTYPE_I64 = 11,
+  RESHARD_DTYPE_FP4_E2M1 = 12, /* two to a byte: group-scaled matrices only, no layout takes it */
 } reshard_dtype_t;
 
 typedef struct reshard_layout_s* reshard_layout_t; /* immutable after create */
@@ -556,12 +557,13 @@ void reshard_plan_destroy(reshard_plan_t plan);
 
 typedef struct reshard_matrix {
   int64_t rows, cols;   /* at most 2^30 each */
-  int32_t dtype;        /* F32, BF16, F16 (plain) or FP8_E4M3, FP8_E5M2 (block-scaled) */
-  int32_t block_rows;   /* 0 (plain), 1 or 128 (block-scaled) */
+  int32_t dtype;        /* F32, BF16, F16 (plain), FP8_E4M3, FP8_E5M2 (block-scaled) or
+                           FP4_E2M1 (group-scaled, below) */
+  int32_t block_rows;   /* 0 (plain), 1 or 128 (block-scaled), 1 (group-scaled) */
   void* data;
   int64_t row_stride;   /* elements between rows */
-  void* scales;         /* one byte per block, NULL for a plain matrix */
-  int64_t scale_stride; /* bytes between rows of blocks */
+  void* scales;         /* one byte per block or group, NULL for a plain matrix */
+  int64_t scale_stride; /* bytes between rows of blocks or groups */
 } reshard_matrix_t;
 
 /*
@@ -638,6 +640,142 @@ reshard_status_t reshard_block_grad(const reshard_matrix_t* dy, const reshard_ma
                                     int64_t workspace_bytes, void* stream);
 reshard_status_t reshard_block_grad_workspace(const reshard_matrix_t* dy, const reshard_matrix_t* x,
                                               const reshard_matrix_t* dw, int64_t* bytes);
+
+/*
+ * Group-scaled 4-bit matrices: the weights of a 4-bit inference layout, and the
+ * products of activations with them.
+ *
+ * Format.  A group-scaled matrix holds one 4-bit float (FP4_E2M1: 0, 1/2, 1, 3/2,
+ * 2, 3, 4, 6 and their negatives) per element and one scale byte b per group of 32
+ * columns of a row (the last group of a row may be short).  The element stands for
+ * q * 2^(b - 127); b = 255 is NaN.  Scales are powers of two for the reasons given
+ * for block-scaled matrices.
+ *   data    two elements a byte, the even column in the low half; row r at
+ *           data + r * row_stride / 2; 16-byte aligned, row_stride (in elements) a
+ *           multiple of 32 and at least the columns rounded up to 32.  The elements
+ *           between the last column and that multiple of 32 must be zero
+ *           (reshard_group_quantize writes them so): products read them.
+ *   scales  group (r, g) at scales + r * scale_stride + g; any alignment,
+ *           scale_stride >= ceil(cols / 32).
+ * reshard_matrix_t describes it with dtype FP4_E2M1 and block_rows 1.
+ *
+ * What is said above of block-scaled calls (streams, capture, memory, overlaps,
+ * matrices with no elements, fixed order of sums, errors) holds for the calls here
+ * and for those of the experts below: each is one to three kernel launches (more
+ * where the counts of pieces pass 2^31).
+ */
+#define RESHARD_GROUP 32
+
+/*
+ * Quantize the plain matrix src into the group-scaled dst of the same shape.  With
+ * amax the largest magnitude of a group its exponent is the smallest e >= -127 with
+ * amax <= 6 * 2^e (0 for a group of zeros), its scale byte e + 127 and each element
+ * x / 2^e rounded to nearest, ties to even.  The format has no infinity and no NaN:
+ * a group with an element that is not finite gets the scale byte 255 and zeros, all
+ * of it NaN.  Padding of the last group is written as zero; bytes beyond it, and
+ * rows beyond the matrices', are left as they were.
+ */
+reshard_status_t reshard_group_quantize(const reshard_matrix_t* src, const reshard_matrix_t* dst, void* stream);
+
+/* Write the values a group-scaled matrix stands for into the plain matrix dst of the
+ * same shape, each rounded once (to nearest, ties to even; exact for F32 and BF16). */
+reshard_status_t reshard_group_dequantize(const reshard_matrix_t* src, const reshard_matrix_t* dst, void* stream);
+
+/*
+ * out[m, n] = sum over k of a[m, k] * b[n, k]: the projection of plain activations a
+ * by a group-scaled weight b stored output features first.  a is used unrounded: an
+ * F16 or F32 value is cut into two or three bfloat16 parts that add up to it, each
+ * multiplied exactly.  Sums are held in binary32 and rounded once to out's type,
+ * which is plain and need not be a's (terms and parts that stay below 2^-126, where
+ * the matrix instructions have no bits, may be lost).  An infinite element, or a sum
+ * past binary32, gives an infinity or a NaN, as in floating point.
+ * workspace: device memory of at least reshard_group_matmul_workspace bytes (0: may
+ * be NULL), 16-byte aligned, not shared with a call that may run at the same time.
+ * Its contents need no preparation.
+ */
+reshard_status_t reshard_group_matmul(const reshard_matrix_t* a, const reshard_matrix_t* b,
+                                      const reshard_matrix_t* out, void* workspace, int64_t workspace_bytes,
+                                      void* stream);
+/* Bytes of workspace reshard_group_matmul needs for matrices of these shapes and
+ * types.  Host only: of the pointers only data's alignment matters, and NULL stands
+ * for an aligned one. */
+reshard_status_t reshard_group_matmul_workspace(const reshard_matrix_t* a, const reshard_matrix_t* b,
+                                                const reshard_matrix_t* out, int64_t* bytes);
+
+/*
+ * Mixtures of experts: tokens sorted by the experts that a router chose for them,
+ * the experts' products, and the way back.  A token has 1 to 64 choices, each an
+ * expert's number.  A rank that holds the experts first .. first + experts - 1 makes
+ * a row for each choice of one of them, expert after expert and, for one expert, in
+ * the order of the choices (token 0's first).  Choices of other experts (negative
+ * numbers among them: a choice left out) have no row.
+ *   offsets[experts + 1]        the rows of held expert e are offsets[e] .. offsets[e + 1] - 1;
+ *                               offsets[0] is 0
+ *   position[tokens * choices]  the row of choice j of token t at t * choices + j, or -1
+ * All of these are 4-byte aligned device arrays of int32.  The calls that read them
+ * trust nothing: a position below zero or at or past the rows of the matrix it
+ * refers to stands for no row, and offsets are cut to the rows there are.  Positions
+ * must be distinct (as reshard_expert_sort writes them): where two choices name one
+ * row, which of them it receives is not determined.
+ */
+#define RESHARD_MAX_EXPERTS 1024
+#define RESHARD_MAX_CHOICES 64
+
+/*
+ * Offsets and positions from the choices ids[tokens * choices] (I32 or I64,
+ * contiguous, aligned to their type).  1 <= experts <= 1024, tokens * choices <=
+ * 2^30.  The order is the same at every call (ties cannot be: a choice is a place).
+ * workspace as for reshard_group_matmul, of reshard_expert_sort_workspace bytes.
+ */
+reshard_status_t reshard_expert_sort(const void* ids, int ids_dtype, int64_t tokens, int choices, int64_t first,
+                                     int64_t experts, int32_t* offsets, int32_t* position, void* workspace,
+                                     int64_t workspace_bytes, void* stream);
+reshard_status_t reshard_expert_sort_workspace(int64_t tokens, int choices, int64_t experts, int64_t* bytes);
+
+/* rows[position[t, j], :] = x[t, :]: each token's row copied, bit for bit, to the rows
+ * of its choices.  rows is plain, of x's type and columns; rows that no choice has
+ * are left as they were.  Its gradient is reshard_expert_combine without weights. */
+reshard_status_t reshard_expert_gather(const reshard_matrix_t* x, const int32_t* position, int choices,
+                                       const reshard_matrix_t* rows, void* stream);
+
+/*
+ * out[t, :] = sum over j of weights[t, j] * rows[position[t, j], :], over the choices
+ * that have a row, in the order of j, products and sums in binary32 (fused or
+ * rounded one after the other), rounded once.  A token without any gets zeros.  rows and out are plain, of one type and of
+ * the same columns; weights is a plain matrix (tokens x choices, any type), or NULL
+ * for weights of 1 (out is then the gradient of reshard_expert_gather's x from that of
+ * its rows).
+ */
+reshard_status_t reshard_expert_combine(const reshard_matrix_t* rows, const int32_t* position, int choices,
+                                        const reshard_matrix_t* weights, const reshard_matrix_t* out, void* stream);
+
+/*
+ * Gradients of reshard_expert_combine from that of its out:
+ *   drows[position[t, j], :] = weights[t, j] * dout[t, :], rounded once; rows that no
+ *                              choice has are left as they were
+ *   dweights[t, j]           = sum over columns of dout[t, :] * rows[position[t, j], :],
+ *                              in binary32, rounded once; 0 for a choice without a row
+ * drows is plain, of dout's type; dweights is plain, of any type.  Either may be NULL,
+ * not both; without dweights rows is not looked at and may be NULL.
+ */
+reshard_status_t reshard_expert_combine_grad(const reshard_matrix_t* dout, const reshard_matrix_t* rows,
+                                             const int32_t* position, int choices, const reshard_matrix_t* weights,
+                                             const reshard_matrix_t* drows, const reshard_matrix_t* dweights,
+                                             void* stream);
+
+/*
+ * reshard_group_matmul with a weight for each expert: row r of out, offsets[e] <= r <
+ * offsets[e + 1], is row r of a times expert e's weight.  b holds the experts' weights one
+ * below the other (experts * n rows, n the columns of out).  offsets is as
+ * reshard_expert_sort writes it: increasing.  Rows of out that no expert has are left as
+ * they were, and those of a are not used.  Everything else is as for
+ * reshard_group_matmul.
+ */
+reshard_status_t reshard_expert_matmul(const reshard_matrix_t* a, const reshard_matrix_t* b, const int32_t* offsets,
+                                       int64_t experts, const reshard_matrix_t* out, void* workspace,
+                                       int64_t workspace_bytes, void* stream);
+reshard_status_t reshard_expert_matmul_workspace(const reshard_matrix_t* a, const reshard_matrix_t* b,
+                                                 int64_t experts, const reshard_matrix_t* out, int64_t* bytes);
 
 /* Message of the calling thread's last failed call ("" if none).  Valid until its next call. */
 const char* reshard_last_error(void);
