@@ -20,7 +20,7 @@ INCLUDE = os.path.join(REPO_DIR, "include")
 LIB_PATH = os.path.join(PKG_DIR, "libreshard.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("plan.cpp", "kernel.hip", "reshard.hip", "checks.cpp",
                                            "blocks.hip", "block_quantize.hip", "block_matmul.hip", "block_grad.hip",
-                                           "groups.hip", "group_quantize.hip", "group_matmul.hip",
+                                           "groups.hip", "group_quantize.hip", "group_matmul.hip", "group_tiles.hip",
                                            "expert_route.hip")]
 
 # Packed-fp32 instructions are kept out of every HIP object; the copy kernel does

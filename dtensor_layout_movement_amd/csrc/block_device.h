@@ -119,6 +119,35 @@ template <typename T, int N> __device__ __forceinline__ void store_stream(T* p, 
   }
 }
 
+template <int N> struct Index {
+  static constexpr int value = N;
+};
+template <int N, typename F> __device__ __forceinline__ void for_each_index(F f) {
+  if constexpr (N > 0) {
+    for_each_index<N - 1>(f);
+    f(Index<N - 1>{});
+  }
+}
+
+// Where 16-byte chunk `chunk` of row `row` of a tile lies, rows 128 bytes apart in LDS: 16
+// rows' reads of one chunk fall into distinct banks.
+__device__ __forceinline__ int slot_of(int row, int chunk) { return chunk ^ ((row >> 1) & 7); }
+
+// Four neighbouring results, of which `left` are inside the row.
+template <int DT>
+__device__ __forceinline__ void store4(typename Elem<DT>::type* p, const f32x4& v, int left) {
+  Pack<typename Elem<DT>::type, 4> r;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) r.v[e] = Elem<DT>::down(v[e]);
+  if (left >= 4) {
+    store_pack<typename Elem<DT>::type, 4>(p, r);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < left) p[e] = r.v[e];
+  }
+}
+
 // 2^(b - 127) of a scale byte (255: NaN, 0: the subnormal 2^-127).
 __device__ __forceinline__ float scale_value(uint32_t b) {
   const uint32_t bits = b == 0 ? 0x00400000u : b == 255 ? 0x7fc00000u : b << 23;

@@ -55,21 +55,6 @@ __device__ __forceinline__ f32x4 step128(const i32x8& x, uint32_t sx, const i32x
   return acc;
 }
 
-// Four neighbouring results, of which `left` are inside the row.
-template <int DT>
-__device__ __forceinline__ void store4(typename Elem<DT>::type* p, const f32x4& v, int left) {
-  Pack<typename Elem<DT>::type, 4> r;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) r.v[e] = Elem<DT>::down(v[e]);
-  if (left >= 4) {
-    store_pack<typename Elem<DT>::type, 4>(p, r);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (e < left) p[e] = r.v[e];
-  }
-}
-
 // A lane's 32 bytes of a row's 128: pieces `part` and `part` + 4 of 16 bytes, so that
 // four lanes read 64 neighbouring bytes at a time (the order within a step only
 // has to be the same on both sides).
@@ -205,7 +190,6 @@ int rows_waves(int64_t groups, int64_t blocks) {
 // SIMD and nothing to run while it waits: 473 us for 442.  A load to LDS writes lane
 // order, so the permutation is made on the address that each lane loads.
 // 128 x 128 tiles, two workgroups a CU: 512 x 14336 x 4096 45 us.
-__device__ __forceinline__ int slot_of(int row, int chunk) { return chunk ^ ((row >> 1) & 7); }
 
 // Moves a tile's rows, 128 bytes from column byte `col` of each, into `to`.
 template <int ROWS, int THREADS>
@@ -261,16 +245,6 @@ template <int FRAGMENTS> __device__ __forceinline__ int scale_place(int r) {
 }
 
 constexpr uint32_t kBand = 8;
-
-template <int N> struct Index {
-  static constexpr int value = N;
-};
-template <int N, typename F> __device__ __forceinline__ void for_each_index(F f) {
-  if constexpr (N > 0) {
-    for_each_index<N - 1>(f);
-    f(Index<N - 1>{});
-  }
-}
 
 // One tile, rows from m0 and columns from n0 on, within the caller's LDS: two
 // buffers of (BM + BN) * 128 bytes and the scales of eight steps.

@@ -14,12 +14,19 @@ inline int64_t groups_of(int64_t cols) { return ceil_div(cols, kGroup); }
 hipError_t launch_group_quantize(const reshard_matrix_t& src, const reshard_matrix_t& dst, hipStream_t stream);
 hipError_t launch_group_dequantize(const reshard_matrix_t& src, const reshard_matrix_t& dst, hipStream_t stream);
 
-// How a product by 4-bit weights runs.
+// How a product by 4-bit weights runs: workspace bytes and launches.
 struct GroupPlan {
-  int waves = 0;       // of a workgroup
-  int64_t slots = 0;   // row chunks, at most
-  int64_t groups = 0;  // workgroups
-  int64_t bytes() const { return 0; }
+  enum Form { kRows, kTiles64, kTiles128, kTiles256 };
+  Form form = kRows;
+  int waves = 0;                  // of a workgroup (kRows)
+  int64_t groups = 0;             // workgroups of the product
+  uint32_t steps = 0;             // of a tile's contraction, and of one part of a's
+  uint32_t part_steps = 0;
+  int splits = 1;                 // workgroups that share a tile's contraction (kTiles64)
+  uint32_t steps_per_split = 0;
+  int64_t planes = 0;             // bytes of a's bfloat16 parts in the workspace (0: read as it lies)
+  int64_t parts = 0;              // bytes of the splits' sums
+  int64_t bytes() const { return planes + parts; }
 };
 // `experts` matrices of b.rows / experts rows each; 0: b is one matrix for all rows of a.
 GroupPlan plan_group_matmul(const reshard_matrix_t& a, const reshard_matrix_t& b, int64_t experts,
@@ -27,6 +34,11 @@ GroupPlan plan_group_matmul(const reshard_matrix_t& a, const reshard_matrix_t& b
 hipError_t launch_group_matmul(const GroupPlan& plan, const reshard_matrix_t& a, const reshard_matrix_t& b,
                                const int32_t* offsets, int64_t experts, const reshard_matrix_t& out, void* workspace,
                                hipStream_t stream);
+
+// The tiled forms of it.
+hipError_t launch_group_tiles(const GroupPlan& plan, const reshard_matrix_t& a, const reshard_matrix_t& b,
+                              const int32_t* offsets, int64_t experts, const reshard_matrix_t& out, void* workspace,
+                              hipStream_t stream);
 
 constexpr int kMaxExperts = RESHARD_MAX_EXPERTS;
 constexpr int64_t kMaxChosen = int64_t(1) << 30;  // tokens times choices
