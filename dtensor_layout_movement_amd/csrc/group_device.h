@@ -66,8 +66,14 @@ __device__ __forceinline__ bool find_tile(const int32_t* offsets, int experts, i
   }
 }
 
-// Eight 4-bit elements times a power of two as bfloat16: exact in bfloat16's normal
-// range (two significant bits).
+// The scale of scale byte `at` of a word, as the conversions take it: they read its exponent
+// only, of which 0 is 2^-127 and 255 NaN.
+__device__ __forceinline__ float scale_of(uint32_t word, int at) {
+  const uint32_t exponent = at < 3 ? word << (23 - 8 * at) : word >> 1;
+  return __builtin_bit_cast(float, exponent & 0x7f800000u);
+}
+
+// Eight 4-bit elements times a power of two as bfloat16: exact (two significant bits).
 __device__ __forceinline__ bf16x8 widen8_fp4(uint32_t q, float scale) {
   bf16x2 p[4];
   p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 0);
@@ -96,17 +102,9 @@ __device__ __forceinline__ uint32_t take_part(float* x) {
   return part >> 16;
 }
 
-// Eight elements of a row from column c on, zero past `cols`, as parts.
-template <int DT, bool GUARD>
-__device__ __forceinline__ void load_parts(const typename Elem<DT>::type* p, int c, int cols, bf16x8 (&y)[Parts<DT>::count]) {
-  typedef typename Elem<DT>::type T;
-  Pack<T, 8> v;
-  if (!GUARD || c + 8 <= cols) {
-    v = load_pack<T, 8>(p + c);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v.v[i] = c + i < cols ? p[c + i] : T(0.f);
-  }
+// Eight elements as parts.
+template <int DT>
+__device__ __forceinline__ void split8(const Pack<typename Elem<DT>::type, 8>& v, bf16x8 (&y)[Parts<DT>::count]) {
   if constexpr (DT == RESHARD_DTYPE_BF16) {
     __builtin_memcpy(&y[0], &v, sizeof(v));
   } else {
@@ -124,6 +122,20 @@ __device__ __forceinline__ void load_parts(const typename Elem<DT>::type* p, int
       __builtin_memcpy(&y[n], w, sizeof(w));
     }
   }
+}
+
+// Eight elements of a row from column c on, zero past `cols`, as parts.
+template <int DT>
+__device__ __forceinline__ void load_parts(const typename Elem<DT>::type* p, int c, int cols, bf16x8 (&y)[Parts<DT>::count]) {
+  typedef typename Elem<DT>::type T;
+  Pack<T, 8> v;
+  if (c + 8 <= cols) {
+    v = load_pack<T, 8>(p + c);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v.v[i] = c + i < cols ? p[c + i] : T(0.f);
+  }
+  split8<DT>(v, y);
 }
 
 }  // namespace rs

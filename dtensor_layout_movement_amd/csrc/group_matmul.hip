@@ -8,20 +8,37 @@
 namespace rs {
 namespace {
 
-// A workgroup makes 16 columns of out for a chunk of up to 16 rows; its waves take the
-// contraction in blocks of 128 columns in turn and their sums are joined through LDS in
-// wave order.  Lane (row r, quarter q) of the 16 x 16 x 32 instruction's operands
-// holds all 32 columns of group 4 k + q of its row: 16 bytes of the weight with one
-// scale, used by four instructions of 8 columns each (the order within a block only has
-// to be the same on both sides).
-constexpr int kRowsHeight = 16, kMaxWaves = 16;
+// Four words of four neighbouring lane groups of 16, exchanged: word j of group q was word q
+// of group j.
+__device__ __forceinline__ i32x4 exchange(const i32x4& v) {
+  const auto a = __builtin_amdgcn_permlane32_swap(uint32_t(v[0]), uint32_t(v[2]), false, false);
+  const auto b = __builtin_amdgcn_permlane32_swap(uint32_t(v[1]), uint32_t(v[3]), false, false);
+  const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+  const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+  return i32x4{int(c[0]), int(c[1]), int(d[0]), int(d[1])};
+}
 
-template <int SRC, int DT>
+// A workgroup makes 16 NT columns of out for a chunk of up to 16 rows; its waves take the
+// contraction in runs of kRun blocks of 128 columns in turn and their sums are joined
+// through LDS in wave order.  An instruction multiplies one group of 32 columns: lane (row
+// r, quarter q) of its operands holds columns 8 q to 8 q + 7 of the group.  So that a load
+// reads as many neighbouring bytes of a row as it can (what a load costs the first cache is
+// its lines), the quarters read 64 bytes of a's row together, group by group, and the whole
+// block's 64 bytes of a weight's row, which they then exchange; the 16 scale bytes of a
+// run's row are one load.
+#ifndef MAXW
+#define MAXW 8
+#endif
+constexpr int kRowsHeight = 16, kMaxWaves = MAXW, kRun = 4, kBlockCols = 4 * kGroup;
+
+template <int SRC, int DT, int NT>
 __global__ __launch_bounds__(64 * kMaxWaves) void group_rows(const typename Elem<SRC>::type* a, int64_t a_stride, int rows,
                                                              int cols, Weight b, const int32_t* offsets, int experts,
                                                              uint32_t n_tiles, typename Elem<DT>::type* out,
                                                              int64_t out_stride) {
-  __shared__ f32x4 sums[kMaxWaves * 64];
+  typedef typename Elem<SRC>::type S;
+  constexpr int kParts = Parts<SRC>::count;
+  extern __shared__ __align__(16) f32x4 sums[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int waves = blockDim.x >> 6;
   Chunk c;
@@ -34,50 +51,116 @@ __global__ __launch_bounds__(64 * kMaxWaves) void group_rows(const typename Elem
     c = Chunk{0, first, min(first + kRowsHeight, rows)};
     n_tile = id % n_tiles;
   }
-  const int n0 = int(n_tile) * 16, part = lane >> 4;
-  const int64_t rb = int64_t(c.expert) * b.rows + min(n0 + (lane & 15), b.rows - 1);
-  const uint8_t* pb = b.data + rb * b.stride;
-  const uint8_t* sb = b.scales + rb * b.scale_stride;
-  const typename Elem<SRC>::type* pa = a + int64_t(min(c.first + (lane & 15), c.last - 1)) * a_stride;
+  const int n0 = int(n_tile) * (16 * NT), part = lane >> 4;
+  const uint8_t *pb[NT], *sb[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const int64_t rb = int64_t(c.expert) * b.rows + min(n0 + i * 16 + (lane & 15), b.rows - 1);
+    pb[i] = b.data + rb * b.stride;
+    sb[i] = b.scales + rb * b.scale_stride;
+  }
+  const S* pa = a + int64_t(min(c.first + (lane & 15), c.last - 1)) * a_stride;
   const int groups = (cols + kGroup - 1) / kGroup;
-  f32x4 acc{0.f, 0.f, 0.f, 0.f};
-  for (int k = wave * 4; k < groups; k += waves * 4) {
-    const int g = k + part, at = min(g, groups - 1);
-    const i32x4 q = *reinterpret_cast<const i32x4*>(pb + at * (kGroup / 2));
-    const float scale = scale_value(sb[at]);
-    bf16x8 y[4][Parts<SRC>::count];
-    if ((k + 4) * kGroup <= cols) {
+  const int full = cols / kBlockCols >= kRun ? cols / kBlockCols : 0;  // blocks taken in runs
+
+  f32x4 acc[NT];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) load_parts<SRC, false>(pa, g * kGroup + j * 8, cols, y[j]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) load_parts<SRC, true>(pa, g * kGroup + j * 8, cols, y[j]);
-    }
+  for (int i = 0; i < NT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const auto multiply = [&](int i, const i32x4& q, uint32_t scales, const bf16x8 (&y)[4][kParts]) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const bf16x8 w = widen8_fp4(uint32_t(q[j]), scale);
+      const bf16x8 w = widen8_fp4(uint32_t(q[j]), scale_of(scales, j));
 #pragma unroll
-      for (int n = 0; n < Parts<SRC>::count; ++n)
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, y[j][n], acc, 0, 0, 0);
+      for (int n = 0; n < kParts; ++n) acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, y[j][n], acc[i], 0, 0, 0);
+    }
+  };
+
+  // A wave's run: blocks k to k + kRun - 1, the last run moved back to end with the last block.
+  i32x4 q[kRun][NT];
+  Pack<uint32_t, kRun> s[NT];
+  const auto load_scales = [&](int k) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) s[i] = load_pack<uint32_t, kRun>(reinterpret_cast<const uint32_t*>(sb[i] + k * 4));
+  };
+  const auto load_block = [&](int u, int k) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+      q[u][i] = *reinterpret_cast<const i32x4*>(pb[i] + (int64_t(k + u) * (kBlockCols / 2) + part * 16));
+  };
+  struct Raw {
+    Pack<S, 8> v[4];
+  };
+  const auto load_a = [&](Raw& r, int k) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.v[j] = load_pack<S, 8>(pa + (k * kBlockCols + j * kGroup + part * 8));
+  };
+  for (int at = wave * kRun; at < full; at += waves * kRun) {
+    const int k = min(at, full - kRun);
+    load_scales(k);
+#pragma unroll
+    for (int u = 0; u < kRun; ++u) load_block(u, k);
+    Raw x, x_next;
+    load_a(x, k);
+#pragma unroll
+    for (int u = 0; u < kRun; ++u) {
+      if (u + 1 < kRun) load_a(x_next, k + u + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      if (k + u >= at) {  // not the wave's before
+        bf16x8 y[4][kParts];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) split8<SRC>(x.v[j], y[j]);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) multiply(i, exchange(q[u][i]), s[i].v[u], y);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      x = x_next;
     }
   }
-  sums[wave * 64 + lane] = acc;
+  // what no run takes: the columns past the last whole block, or few blocks
+  for (int k = full + wave; k * 4 < groups; k += waves) {
+    const int g = min(k * 4 + part, groups - 1);
+    bf16x8 y[4][kParts];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) load_parts<SRC>(pa, k * kBlockCols + j * kGroup + part * 8, cols, y[j]);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      uint32_t scales = 0;  // of groups that there are not, one that is finite
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (k * 4 + j < groups) scales |= uint32_t(sb[i][k * 4 + j]) << (8 * j);
+      multiply(i, exchange(*reinterpret_cast<const i32x4*>(pb[i] + int64_t(g) * 16)), scales, y);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NT; ++i) sums[(wave * NT + i) * 64 + lane] = acc[i];
   __syncthreads();
-  if (wave) return;
-  for (int w = 1; w < waves; ++w) acc += sums[w * 64 + lane];
-  const int m = c.first + (lane & 15), n = n0 + part * 4;
-  if (m < c.last) store4<DT>(out + m * out_stride + n, acc, b.rows - n);
+  for (int i = wave; i < NT; i += waves) {
+    f32x4 sum = sums[i * 64 + lane];
+    for (int w = 1; w < waves; ++w) sum += sums[(w * NT + i) * 64 + lane];
+    const int m = c.first + (lane & 15), n = n0 + i * 16 + part * 4;
+    if (m < c.last) store4<DT>(out + m * out_stride + n, sum, b.rows - n);
+  }
+}
+
+template <int SRC, int DT, int NT>
+hipError_t rows_as(const GroupPlan& plan, const reshard_matrix_t& a, const reshard_matrix_t& b, const int32_t* offsets,
+                   int64_t experts, const reshard_matrix_t& out, hipStream_t stream) {
+  const Weight w{static_cast<const uint8_t*>(b.data), b.row_stride / 2, static_cast<const uint8_t*>(b.scales),
+                 b.scale_stride, int(out.cols)};
+  group_rows<SRC, DT, NT><<<dim3(uint32_t(plan.groups)), 64 * plan.waves, plan.waves * NT * 64 * sizeof(f32x4), stream>>>(
+      static_cast<const typename Elem<SRC>::type*>(a.data), a.row_stride, int(a.rows), int(a.cols), w, offsets,
+      int(experts), uint32_t(ceil_div(out.cols, 16 * NT)), static_cast<typename Elem<DT>::type*>(out.data), out.row_stride);
+  return hipGetLastError();
 }
 
 template <int SRC, int DT>
 hipError_t product_as(const GroupPlan& plan, const reshard_matrix_t& a, const reshard_matrix_t& b, const int32_t* offsets,
                       int64_t experts, const reshard_matrix_t& out, hipStream_t stream) {
-  const Weight w{static_cast<const uint8_t*>(b.data), b.row_stride / 2, static_cast<const uint8_t*>(b.scales),
-                 b.scale_stride, int(out.cols)};
-  group_rows<SRC, DT><<<dim3(uint32_t(plan.groups)), 64 * plan.waves, 0, stream>>>(
-      static_cast<const typename Elem<SRC>::type*>(a.data), a.row_stride, int(a.rows), int(a.cols), w, offsets,
-      int(experts), uint32_t(ceil_div(out.cols, 16)), static_cast<typename Elem<DT>::type*>(out.data), out.row_stride);
-  return hipGetLastError();
+  switch (plan.n_tiles) {
+    case 1: return rows_as<SRC, DT, 1>(plan, a, b, offsets, experts, out, stream);
+    case 2: return rows_as<SRC, DT, 2>(plan, a, b, offsets, experts, out, stream);
+    default: return rows_as<SRC, DT, 4>(plan, a, b, offsets, experts, out, stream);
+  }
 }
 
 template <int SRC>
@@ -136,10 +219,20 @@ GroupPlan plan_group_matmul(const reshard_matrix_t& a, const reshard_matrix_t& b
     }
     return p;
   }
-  p.groups = tiles(kRowsHeight, 16);
-  const int64_t blocks = ceil_div(a.cols, 4 * kGroup);
-  p.waves = 4;
-  while (p.waves < kMaxWaves && p.groups * p.waves < 4096 && p.waves < blocks) p.waves *= 2;
+  const int64_t runs = std::max<int64_t>(1, ceil_div(a.cols / (4 * kGroup), kRun));
+#ifndef NTMIN
+#define NTMIN 448
+#endif
+#ifndef NTMAX
+#define NTMAX 4
+#endif
+  p.n_tiles = 1;
+  while (p.n_tiles < NTMAX && tiles(kRowsHeight, 32 * p.n_tiles) >= NTMIN) p.n_tiles *= 2;
+  p.groups = tiles(kRowsHeight, 16 * p.n_tiles);
+#ifndef MAXW
+#define MAXW 16
+#endif
+  p.waves = int(ceil_div(runs, ceil_div(runs, MAXW)));
   return p;
 }
 

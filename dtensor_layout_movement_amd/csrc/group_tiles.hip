@@ -118,7 +118,7 @@ __device__ __forceinline__ void make_tile(const Rows& a, const Weight& b, int gr
   const auto step = [&](const uint8_t* tile, const uint64_t (&s)[kN], int bit, auto fill, auto turn) {
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      const float f = scale_value(uint32_t(s[i] >> ((bit + 8 * (part >> 1)) & 63)) & 255);
+      const float f = scale_of(uint32_t(s[i] >> ((bit + 8 * (part >> 1)) & 63)), 0);
       w[i].half[0] = widen8_fp4(uint32_t(raw[i][0]), f);
       w[i].half[1] = widen8_fp4(uint32_t(raw[i][1]), f);
     }
@@ -230,7 +230,7 @@ __global__ __launch_bounds__(256) void split_rows(const typename Elem<SRC>::type
   if (i >= items) return;
   const uint32_t row = quotient(i, chunks), chunk = i - row * chunks.d;
   bf16x8 y[Parts<SRC>::count];
-  load_parts<SRC, true>(a + int64_t(row) * stride, int(chunk) * 8, cols, y);
+  load_parts<SRC>(a + int64_t(row) * stride, int(chunk) * 8, cols, y);
 #pragma unroll
   for (int n = 0; n < Parts<SRC>::count; ++n)
     *reinterpret_cast<bf16x8*>(to + int64_t(row) * to_stride + (uint32_t(n) * chunks.d + chunk) * 16) = y[n];

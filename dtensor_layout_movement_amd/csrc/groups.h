@@ -18,7 +18,8 @@ hipError_t launch_group_dequantize(const reshard_matrix_t& src, const reshard_ma
 struct GroupPlan {
   enum Form { kRows, kTiles64, kTiles128, kTiles256 };
   Form form = kRows;
-  int waves = 0;                  // of a workgroup (kRows)
+  int waves = 0;                  // of a workgroup, and its tiles of 16 columns (kRows)
+  int n_tiles = 1;
   int64_t groups = 0;             // workgroups of the product
   uint32_t steps = 0;             // of a tile's contraction, and of one part of a's
   uint32_t part_steps = 0;
