@@ -94,27 +94,42 @@ __global__ __launch_bounds__(64 * kMaxWaves) void group_rows(const typename Elem
 #pragma unroll
     for (int j = 0; j < 4; ++j) r.v[j] = load_pack<S, 8>(pa + (k * kBlockCols + j * kGroup + part * 8));
   };
-  for (int at = wave * kRun; at < full; at += waves * kRun) {
+  // With NEXT the wave's next run, from block `to` on, is asked for as this one is used up.
+  Raw x[kRun];
+  const auto run = [&](int at, int to, auto next) {
+    const int k = min(at, full - kRun);
+    Pack<uint32_t, kRun> s_now[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) s_now[i] = s[i];
+#pragma unroll
+    for (int u = 0; u < kRun; ++u) {
+      if (k + u >= at) {  // not the run's before
+        bf16x8 y[4][kParts];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) split8<SRC>(x[u].v[j], y[j]);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) multiply(i, exchange(q[u][i]), s_now[i].v[u], y);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (decltype(next)::value) {
+        if (u == 0) load_scales(to);
+        load_block(u, to);
+        load_a(x[u], to + u);
+      }
+    }
+  };
+  int at = wave * kRun;
+  if (at < full) {
     const int k = min(at, full - kRun);
     load_scales(k);
 #pragma unroll
-    for (int u = 0; u < kRun; ++u) load_block(u, k);
-    Raw x, x_next;
-    load_a(x, k);
-#pragma unroll
     for (int u = 0; u < kRun; ++u) {
-      if (u + 1 < kRun) load_a(x_next, k + u + 1);
-      __builtin_amdgcn_sched_barrier(0);
-      if (k + u >= at) {  // not the wave's before
-        bf16x8 y[4][kParts];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) split8<SRC>(x.v[j], y[j]);
-#pragma unroll
-        for (int i = 0; i < NT; ++i) multiply(i, exchange(q[u][i]), s[i].v[u], y);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-      x = x_next;
+      load_block(u, k);
+      load_a(x[u], k + u);
     }
+    __builtin_amdgcn_sched_barrier(0);
+    for (; at + waves * kRun < full; at += waves * kRun) run(at, min(at + waves * kRun, full - kRun), Index<1>{});
+    run(at, 0, Index<0>{});
   }
   // what no run takes: the columns past the last whole block, or few blocks
   for (int k = full + wave; k * 4 < groups; k += waves) {
@@ -175,6 +190,12 @@ hipError_t product_from(const GroupPlan& plan, const reshard_matrix_t& a, const 
 
 }  // namespace
 
+#ifndef SPLC
+#define SPLC 2
+#endif
+#ifndef SPLS
+#define SPLS 6
+#endif
 GroupPlan plan_group_matmul(const reshard_matrix_t& a, const reshard_matrix_t& b, int64_t experts,
                             const reshard_matrix_t& out) {
   GroupPlan p;
@@ -197,10 +218,11 @@ GroupPlan plan_group_matmul(const reshard_matrix_t& a, const reshard_matrix_t& b
   if (mean > kRowsHeight && groups_of(a.cols) >= 8 && out.cols && stride <= (int64_t(1) << 22)) {
     if (tiles(256, 256) >= 192 && (!experts || mean >= 192)) {
       p.form = GroupPlan::kTiles256;
-      p.groups = tiles(256, 256);
+      p.whole = experts ? 0 : whole_tiles(tiles(256, 256));
+      p.groups = experts ? tiles(256, 256) : 2 * tiles(256, 256) - p.whole;
     } else if (tiles(128, 128) >= 256 && mean > 64) {
       p.form = GroupPlan::kTiles128;
-      p.groups = tiles(128, 128);
+      p.whole = p.groups = tiles(128, 128);
     } else {
       p.form = GroupPlan::kTiles64;
       p.groups = tiles(64, 128);
@@ -211,10 +233,10 @@ GroupPlan plan_group_matmul(const reshard_matrix_t& a, const reshard_matrix_t& b
     if (!direct) p.planes = round_up(a.rows * parts * part_steps * 128, 256);
     if (p.form == GroupPlan::kTiles64 && !experts) {
       const int64_t t = p.groups;
-      int64_t splits = std::max<int64_t>(1, std::min(2 * kCus / t, ceil_div(p.steps, 6)));
+      int64_t splits = std::max<int64_t>(1, std::min(SPLC * kCus / t, ceil_div(p.steps, SPLS)));
       p.steps_per_split = uint32_t(ceil_div(ceil_div(p.steps, splits), 3) * 3);
       p.splits = int(ceil_div(p.steps, p.steps_per_split));
-      p.groups = t * p.splits;
+      p.whole = p.groups = t * p.splits;
       if (p.splits > 1) p.parts = p.splits * out.rows * round_up(out.cols, 4) * 4;
     }
     return p;

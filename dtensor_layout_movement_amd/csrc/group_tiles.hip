@@ -16,25 +16,28 @@ struct Rows {
   uint32_t chunks;  // of 8 columns that a row has, parts together
 };
 
-constexpr int kStep = 64;  // columns of a step
-constexpr int kRowA = kStep * 2, kRowB = kStep / 2;  // their bytes
+constexpr int kStep = 64;                        // columns of a step
+constexpr int kThree = 3;                         // steps that share a load of the weight
+constexpr int kRowA = kStep * 2, kRowB = kThree * kStep / 2;  // bytes of a row of a step, and of three
 
 // A workgroup makes a BM (rows of a) x BN (rows of b) tile with WM x WN waves.  A step
-// takes 64 columns of both through LDS, loaded straight there (16 bytes a lane) two
-// steps ahead into the third of three buffers: a's rows lie 128 bytes apart, their
-// 16-byte chunks permuted (slot_of), the weight's 32 bytes apart as they are.  A lane
-// (row, quarter q) reads 16 consecutive columns of its row on both sides, 8 for each
-// of two instructions, and widens the weight's to bfloat16, scaled, in registers: one
-// scale of the row's two.  The scales of three steps (6 bytes a row) are loaded into
-// registers three steps ahead, as they lie: a shift here would wait for them.
+// takes 64 columns of a through LDS, loaded straight there (16 bytes a lane) two steps
+// ahead into the third of three buffers; rows lie 128 bytes apart, their 16-byte chunks
+// permuted (slot_of).  The weight goes there three steps at a time, 96 bytes a row, into
+// the other of two buffers: with 32 bytes a row each step, three of four loads found their
+// line still on its way, which holds up the first cache (a third of all cycles of 4096 x
+// 14336 x 4096).  A lane (row, quarter q) reads 16 consecutive columns of its row on both
+// sides, 8 for each of two instructions, and widens the weight's to bfloat16, scaled, in
+// registers: one scale of the row's two.  The scales of three steps (6 bytes a row) are
+// loaded into registers a step ahead, as they lie: a shift there would wait for them.
 template <int DT, int BM, int BN, int WM, int WN>
 __device__ __forceinline__ void make_tile(const Rows& a, const Weight& b, int groups, const Chunk& c, int n0,
                                           uint32_t first, uint32_t last, uint32_t part_steps,
-                                          typename Elem<DT>::type* out, int64_t out_stride, uint8_t* tile0,
-                                          uint8_t* tile1, uint8_t* tile2) {
+                                          typename Elem<DT>::type* out, int64_t out_stride, uint8_t* a0, uint8_t* a1,
+                                          uint8_t* a2, uint8_t* b0, uint8_t* b1) {
   constexpr int kThreads = 64 * WM * WN, kM = BM / WM / 16, kN = BN / WN / 16;
-  constexpr int kLoadsA = BM * 8 / kThreads, kLoadsB = BN * 2 / kThreads, kLoads = kLoadsA + kLoadsB;
-  static_assert(kM > 2 && kThreads % 128 == 0 && BN * 2 % kThreads == 0 && BM * 8 % kThreads == 0, "");
+  constexpr int kLoadsA = BM * 8 / kThreads, kLoadsB = BN * 6 / kThreads;
+  static_assert(kM > 2 && kThreads % 128 == 0 && BN * 6 % kThreads == 0 && BM * 8 % kThreads == 0, "");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN, frow = lane & 15, part = lane >> 4;
   const int m_rows = c.last - c.first, n_rows = min(BN, b.rows - n0);
@@ -46,20 +49,26 @@ __device__ __forceinline__ void make_tile(const Rows& a, const Weight& b, int gr
   // rows of one thread's loads are a multiple of 16 apart: they have one chunk in common
   const uint32_t chunk = uint32_t(slot_of(int(threadIdx.x) >> 3, int(threadIdx.x) & 7));
   const uint32_t off_a = (threadIdx.x >> 3) * uint32_t(a.stride) + chunk * 16;
-  const uint32_t off_b = (threadIdx.x >> 1) * uint32_t(b.stride) + (threadIdx.x & 1) * 16;
-  // Step k of the contraction, step kb of the weight.  (Steps that pad a part of a lie past
-  // the weight's groups: a is zero there, and the weight's last are as good as any.)
-  const uint32_t last_b = uint32_t(groups - 1) / 2;
-  const auto load = [&](uint8_t* to, uint32_t k, uint32_t kb) {
+  const auto load_a = [&](uint8_t* to, uint32_t k) {
     const bool inside = k * 8 + chunk < a.chunks;
 #pragma unroll
     for (int i = 0; i < kLoadsA; ++i)
       load_to_lds(base_a, to + (i * kThreads + wave * 64) * 16,
                   inside ? off_a + uint32_t(i * (kThreads / 8)) * uint32_t(a.stride) : 0x7ffffff0u, k * kRowA);
+  };
+  uint32_t off_b[kLoadsB];
+#pragma unroll
+  for (int i = 0; i < kLoadsB; ++i) {
+    const uint32_t at = threadIdx.x + i * kThreads;
+    off_b[i] = at / 6 * uint32_t(b.stride) + at % 6 * 16;
+  }
+  // Three steps of the weight from step kb on.  (What lies past a row's groups meets zeros of
+  // a; loads past the contraction's last step are made to no use.)
+  const uint32_t last_b = uint32_t(groups - 1) / 6 * 3;
+  const auto load_b = [&](uint8_t* to, uint32_t kb) {
 #pragma unroll
     for (int i = 0; i < kLoadsB; ++i)
-      load_to_lds(base_b, to + BM * kRowA + (i * kThreads + wave * 64) * 16,
-                  off_b + uint32_t(i * (kThreads / 2)) * uint32_t(b.stride), min(kb, last_b) * kRowB);
+      load_to_lds(base_b, to + (i * kThreads + wave * 64) * 16, off_b[i], min(kb, last_b) * (kStep / 2));
   };
 
   const uint8_t* scales = b.scales + row_b0 * b.scale_stride;
@@ -85,7 +94,7 @@ __device__ __forceinline__ void make_tile(const Rows& a, const Weight& b, int gr
 
   // where this lane's chunks lie in a tile: rows 16 apart keep their slots
   const int slot0 = slot_of(frow, 2 * part) * 16, slot1 = slot_of(frow, 2 * part + 1) * 16;
-  const int row_a = (wm * (BM / WM) + frow) * kRowA, row_b = BM * kRowA + (wn * (BN / WN) + frow) * kRowB + part * 8;
+  const int row_a = (wm * (BM / WM) + frow) * kRowA, row_b = (wn * (BN / WN) + frow) * kRowB + part * 8;
   struct Fragment {
     bf16x8 half[2];
   };
@@ -98,9 +107,10 @@ __device__ __forceinline__ void make_tile(const Rows& a, const Weight& b, int gr
   // the weight's columns of a step and the first rows of a, read before the step begins
   i32x2 raw[kN];
   Fragment x;
-  const auto begin = [&](const uint8_t* tile) {
+  const auto begin = [&](const uint8_t* tile, const uint8_t* weight, int third) {
 #pragma unroll
-    for (int i = 0; i < kN; ++i) raw[i] = *reinterpret_cast<const i32x2*>(tile + row_b + i * (16 * kRowB));
+    for (int i = 0; i < kN; ++i)
+      raw[i] = *reinterpret_cast<const i32x2*>(weight + row_b + i * (16 * kRowB) + third * (kStep / 2));
     x = fragment_a(tile, 0);
   };
   Fragment w[kN];
@@ -113,8 +123,8 @@ __device__ __forceinline__ void make_tile(const Rows& a, const Weight& b, int gr
         acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i].half[h], xj.half[h], acc[i][j], 0, 0, 0);
     __builtin_amdgcn_sched_barrier(0);
   };
-  // `fill` asks for the tile two steps on, behind the step's first reads; `turn`, between
-  // the step's last read and its last products, waits for the next tile and reads its first.
+  // `fill` asks for what comes later, behind the step's first reads; `turn`, between the
+  // step's last read and its last products, waits for the next step's and reads its first.
   const auto step = [&](const uint8_t* tile, const uint64_t (&s)[kN], int bit, auto fill, auto turn) {
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
@@ -138,43 +148,62 @@ __device__ __forceinline__ void make_tile(const Rows& a, const Weight& b, int gr
     products(Index<kM - 1>{}, next);
   };
 
-  // In the loop every load is made at every turn, past the last step to no use, so that
-  // their count stays the same and no wait is for more than it has to be.
+  // Every load is made at every turn, past the last step to no use: then the loads under
+  // way behind those that a barrier waits for are known, a's next but one step at least
+  // and, while they are young, the weight's next three.  (Scales come on top of them: a
+  // barrier that waits for more than it has to is no fault.)
   uint32_t kb = first % part_steps, k = first;
-  uint64_t s[kN], s_next[kN];
+  uint64_t s[kN];
   load_scales(s, kb);
   __builtin_amdgcn_sched_barrier(0);
-  load(tile0, first, kb);
-  load(tile1, min(first + 1, last - 1), kb + 1);
-  loads_barrier<kLoads>();
-  begin(tile0);
-  for (; k + 3 <= last; k += 3) {
-    const uint32_t kn = kb + 3 < part_steps ? kb + 3 : 0;  // of the next three
-    const int bit = scales_at(kb);
-    load_scales(s_next, kn);
-    __builtin_amdgcn_sched_barrier(0);
-    step(tile0, s, bit, [&] { load(tile2, k + 2, kb + 2); }, [&] {
-      loads_barrier<kLoads>();  // tile1 has arrived, tile0 has been read
-      begin(tile1);
+  load_b(b0, kb);
+  load_a(a0, first);
+  load_a(a1, min(first + 1, last - 1));
+  loads_barrier<kLoadsA>();
+  begin(a0, b0, 0);
+  uint32_t kn;  // the weight's next three: it starts over for a's next part
+  int bit;
+  const auto first_of = [&](const uint8_t* now, uint8_t* later) {
+    kn = kb + 3 < part_steps ? kb + 3 : 0;
+    bit = scales_at(kb);
+    step(a0, s, bit, [&] { load_a(a2, min(k + 2, last - 1)); load_b(later, kn); }, [&] {
+      loads_barrier<kLoadsA + kLoadsB>();  // a1 has arrived, a0 has been read
+      begin(a1, now, 1);
     });
-    step(tile1, s, bit + 16, [&] { load(tile0, min(k + 3, last - 1), kn); }, [&] {
-      loads_barrier<kLoads>();
-      begin(tile2);
+  };
+  const auto second_of = [&](const uint8_t* now) {
+    step(a1, s, bit + 16, [&] { load_a(a0, min(k + 3, last - 1)); }, [&] {
+      loads_barrier<kLoadsA + kLoadsB>();
+      begin(a2, now, 2);
     });
-    step(tile2, s, bit + 32, [&] { load(tile1, min(k + 4, last - 1), kn + 1); }, [&] {
-      loads_barrier<kLoads>();
-      begin(tile0);
+  };
+  const auto third_of = [&](const uint8_t* later) {
+    step(a2, s, bit + 32, [&] {
+      load_scales(s, kn);  // this step's are in use already
+      __builtin_amdgcn_sched_barrier(0);
+      load_a(a1, min(k + 4, last - 1));
+    }, [&] {
+      loads_barrier<kLoadsA>();  // the next three steps' weight too
+      begin(a0, later, 0);
     });
-#pragma unroll
-    for (int i = 0; i < kN; ++i) s[i] = s_next[i];
     kb = kn;
+    k += 3;
+  };
+  while (k + 6 <= last) {
+    first_of(b0, b1);
+    second_of(b0);
+    third_of(b1);
+    first_of(b1, b0);
+    second_of(b1);
+    third_of(b0);
   }
-  if (k < last)
-    step(tile0, s, scales_at(kb), [] {}, [&] {
-      loads_barrier<0>();
-      begin(tile1);
-    });
-  if (k + 1 < last) step(tile1, s, scales_at(kb) + 16, [] {}, [] {});
+  // (the rest in one line of steps: with branches that join the sums do not stay in place)
+  const uint32_t left = last - k;
+  if (left > 0) first_of(b0, b1);
+  if (left > 1) second_of(b0);
+  if (left > 2) third_of(b1);
+  if (left > 3) first_of(b1, b0);
+  if (left > 4) second_of(b1);
   loads_barrier<0>();  // no load may outlive its use of LDS
 #pragma unroll
   for (int j = 0; j < kM; ++j) {
@@ -193,32 +222,52 @@ __device__ __forceinline__ void make_tile(const Rows& a, const Weight& b, int gr
 // the most in its L2.
 constexpr uint32_t kBand = 8;
 
+// Tiles of 256 rows with at most 128 of them are made as tiles of 128; workgroups from
+// `whole` on, which would leave half of the card idle in the last round, make half a tile
+// each.
 template <int DT, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN, 2) void group_tiles(Rows a, Weight b, int groups, const int32_t* offsets,
                                                                int experts, uint32_t m_tiles, uint32_t n_tiles,
-                                                               uint32_t steps, uint32_t part_steps, uint32_t steps_per_split,
+                                                               uint32_t whole, uint32_t steps, uint32_t part_steps,
+                                                               uint32_t steps_per_split,
                                                                typename Elem<DT>::type* out, int64_t out_stride,
                                                                int64_t split_stride) {
-  constexpr int kBytes = BM * kRowA + BN * kRowB;
-  __shared__ __align__(128) uint8_t tile0[kBytes];
-  __shared__ __align__(128) uint8_t tile1[kBytes];
-  __shared__ __align__(128) uint8_t tile2[kBytes];
+  __shared__ __align__(128) uint8_t a0[BM * kRowA];
+  __shared__ __align__(128) uint8_t a1[BM * kRowA];
+  __shared__ __align__(128) uint8_t a2[BM * kRowA];
+  __shared__ __align__(128) uint8_t b0[BN * kRowB];
+  __shared__ __align__(128) uint8_t b1[BN * kRowB];
   Chunk c;
   uint32_t n_tile, split = 0;
   if (offsets) {
     if (!find_tile(offsets, experts, a.rows, BM, blockIdx.x, n_tiles, &c, &n_tile)) return;
   } else {
     const uint32_t tiles = m_tiles * n_tiles;
-    split = blockIdx.x / tiles;
-    const uint32_t t = run_of(blockIdx.x % tiles, tiles);
+    uint32_t t, half = 2;
+    if (blockIdx.x < whole) {
+      split = blockIdx.x / tiles;
+      t = run_of(blockIdx.x % tiles, min(tiles, whole));
+    } else {
+      const uint32_t i = run_of(blockIdx.x - whole, gridDim.x - whole);
+      t = whole + i / 2;
+      half = i % 2;
+    }
     const uint32_t band = t / (kBand * n_tiles), rows = min(kBand, m_tiles - band * kBand), in = t - band * kBand * n_tiles;
     const int first = int(band * kBand + in % rows) * BM;
     c = Chunk{0, first, min(first + BM, a.rows)};
     n_tile = in / rows;
+    if (half < 2) {
+      c = Chunk{0, first + int(half) * (BM / 2), min(first + int(half + 1) * (BM / 2), a.rows)};
+      if (c.first >= c.last) return;
+    }
   }
   const uint32_t first = split * steps_per_split, last = min(first + steps_per_split, steps);
-  make_tile<DT, BM, BN, WM, WN>(a, b, groups, c, int(n_tile) * BN, first, last, part_steps, out + split * split_stride,
-                                out_stride, tile0, tile1, tile2);
+  if (BM == 256 && c.last - c.first <= BM / 2)
+    make_tile<DT, BM == 256 ? 128 : BM, BN, WM, WN>(a, b, groups, c, int(n_tile) * BN, first, last, part_steps,
+                                                    out + split * split_stride, out_stride, a0, a1, a2, b0, b1);
+  else
+    make_tile<DT, BM, BN, WM, WN>(a, b, groups, c, int(n_tile) * BN, first, last, part_steps, out + split * split_stride,
+                                  out_stride, a0, a1, a2, b0, b1);
 }
 
 // The bfloat16 parts of a's rows, one behind the other, each of `width` columns, zero past
@@ -255,7 +304,8 @@ template <int DT, int BM, int BN, int WM, int WN>
 hipError_t tiles_as(const GroupPlan& plan, const Rows& a, const Weight& b, int groups, const int32_t* offsets,
                     int64_t experts, void* out, int64_t out_stride, int64_t split_stride, hipStream_t stream) {
   group_tiles<DT, BM, BN, WM, WN><<<dim3(uint32_t(plan.groups)), 64 * WM * WN, 0, stream>>>(
-      a, b, groups, offsets, int(experts), uint32_t(ceil_div(a.rows, BM)), uint32_t(ceil_div(b.rows, BN)), plan.steps,
+      a, b, groups, offsets, int(experts), uint32_t(ceil_div(a.rows, BM)), uint32_t(ceil_div(b.rows, BN)),
+      uint32_t(plan.whole), plan.steps,
       plan.part_steps, plan.steps_per_split, static_cast<typename Elem<DT>::type*>(out), out_stride, split_stride);
   return hipGetLastError();
 }

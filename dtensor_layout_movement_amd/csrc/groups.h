@@ -21,6 +21,7 @@ struct GroupPlan {
   int waves = 0;                  // of a workgroup, and its tiles of 16 columns (kRows)
   int n_tiles = 1;
   int64_t groups = 0;             // workgroups of the product
+  int64_t whole = 0;              // of them those that make a whole tile, or a split of one (tiles)
   uint32_t steps = 0;             // of a tile's contraction, and of one part of a's
   uint32_t part_steps = 0;
   int splits = 1;                 // workgroups that share a tile's contraction (kTiles64)
