@@ -85,6 +85,22 @@ __device__ __forceinline__ bf16x8 widen8_fp4(uint32_t q, float scale) {
   return r;
 }
 
+// What a load of 16 bytes a lane costs the first cache are the lines that neighbouring
+// lanes touch: 16 where a quad of lanes reads 64 bytes of one of 16 rows, 64 where
+// neighbouring lanes read different rows.  So rows are read by quads, and what lane 4 r + q
+// read goes to lane r + 16 q, where the matrix instructions take it.
+__device__ __forceinline__ int from_quads() { return int(((threadIdx.x & 15) * 4 + (threadIdx.x >> 4 & 3)) * 4); }
+template <typename T> __device__ __forceinline__ T permuted(const T& v, int from) {
+  static_assert(sizeof(T) % 4 == 0, "");
+  int w[sizeof(T) / 4];
+  __builtin_memcpy(w, &v, sizeof(T));
+#pragma unroll
+  for (int i = 0; i < int(sizeof(T) / 4); ++i) w[i] = __builtin_amdgcn_ds_bpermute(from, w[i]);
+  T r;
+  __builtin_memcpy(&r, w, sizeof(T));
+  return r;
+}
+
 // bfloat16 parts that add up to an element of a: its leading bits, those that follow,
 // and so on, each cut off (so that a part of a finite element is finite).
 template <int DT> struct Parts;

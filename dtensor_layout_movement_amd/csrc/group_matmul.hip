@@ -19,17 +19,19 @@ __device__ __forceinline__ i32x4 exchange(const i32x4& v) {
 }
 
 // A workgroup makes 16 NT columns of out for a chunk of up to 16 rows; its waves take the
-// contraction in runs of kRun blocks of 128 columns in turn and their sums are joined
-// through LDS in wave order.  An instruction multiplies one group of 32 columns: lane (row
-// r, quarter q) of its operands holds columns 8 q to 8 q + 7 of the group.  So that a load
-// reads as many neighbouring bytes of a row as it can (what a load costs the first cache is
-// its lines), the quarters read 64 bytes of a's row together, group by group, and the whole
-// block's 64 bytes of a weight's row, which they then exchange; the 16 scale bytes of a
-// run's row are one load.
-#ifndef MAXW
-#define MAXW 8
-#endif
-constexpr int kRowsHeight = 16, kMaxWaves = MAXW, kRun = 4, kBlockCols = 4 * kGroup;
+// contraction in runs of kRun blocks of 128 columns in turn, the next run's loads under way
+// as one is used up, and their sums are joined through LDS in wave order.  An instruction
+// multiplies one group of 32 columns: lane (row r, quarter q) of its operands holds columns
+// 8 q to 8 q + 7 of the group.  The weight is read by quads of lanes, the block's 64 bytes
+// of a row each, and comes to its lanes through two exchanges; a, of which few rows are
+// often all the same one, is read where it is used.
+//
+// Bound by the weight's bytes where they are many: 128 rows at 64 experts of 2048 x 7168,
+// 437 MB of weights, take 79 us (5.5 TB/s); by a launch and one trip to HBM where they are
+// few: one token through 14336 x 4096, 31 MB, 9.7 us, through 4096 x 14336 7.8.  Read without
+// quads those took 92, 9.3 and 9.0, 16 rows through 4096 x 14336 18.2 for 15.7; with a read by
+// quads too the tokens took 11.0 and 13.5.  Eight waves: 77 tokens' experts 171 for 151.
+constexpr int kRowsHeight = 16, kMaxWaves = 4, kRun = 4, kBlockCols = 4 * kGroup;
 
 template <int SRC, int DT, int NT>
 __global__ __launch_bounds__(64 * kMaxWaves) void group_rows(const typename Elem<SRC>::type* a, int64_t a_stride, int rows,
@@ -51,11 +53,11 @@ __global__ __launch_bounds__(64 * kMaxWaves) void group_rows(const typename Elem
     c = Chunk{0, first, min(first + kRowsHeight, rows)};
     n_tile = id % n_tiles;
   }
-  const int n0 = int(n_tile) * (16 * NT), part = lane >> 4;
+  const int n0 = int(n_tile) * (16 * NT), part = lane >> 4, quad = lane >> 2, in_quad = lane & 3, from = from_quads();
   const uint8_t *pb[NT], *sb[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-    const int64_t rb = int64_t(c.expert) * b.rows + min(n0 + i * 16 + (lane & 15), b.rows - 1);
+    const int64_t rb = int64_t(c.expert) * b.rows + min(n0 + i * 16 + quad, b.rows - 1);
     pb[i] = b.data + rb * b.stride;
     sb[i] = b.scales + rb * b.scale_stride;
   }
@@ -77,15 +79,15 @@ __global__ __launch_bounds__(64 * kMaxWaves) void group_rows(const typename Elem
 
   // A wave's run: blocks k to k + kRun - 1, the last run moved back to end with the last block.
   i32x4 q[kRun][NT];
-  Pack<uint32_t, kRun> s[NT];
+  uint32_t s[NT];  // a quad's lanes hold a run's four words
   const auto load_scales = [&](int k) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i) s[i] = load_pack<uint32_t, kRun>(reinterpret_cast<const uint32_t*>(sb[i] + k * 4));
+    for (int i = 0; i < NT; ++i) s[i] = load_pack<uint32_t, 1>(reinterpret_cast<const uint32_t*>(sb[i] + (k + in_quad) * 4)).v[0];
   };
   const auto load_block = [&](int u, int k) {
 #pragma unroll
     for (int i = 0; i < NT; ++i)
-      q[u][i] = *reinterpret_cast<const i32x4*>(pb[i] + (int64_t(k + u) * (kBlockCols / 2) + part * 16));
+      q[u][i] = *reinterpret_cast<const i32x4*>(pb[i] + (int64_t(k + u) * (kBlockCols / 2) + in_quad * 16));
   };
   struct Raw {
     Pack<S, 8> v[4];
@@ -98,7 +100,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void group_rows(const typename Elem
   Raw x[kRun];
   const auto run = [&](int at, int to, auto next) {
     const int k = min(at, full - kRun);
-    Pack<uint32_t, kRun> s_now[NT];
+    uint32_t s_now[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) s_now[i] = s[i];
 #pragma unroll
@@ -108,7 +110,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void group_rows(const typename Elem
 #pragma unroll
         for (int j = 0; j < 4; ++j) split8<SRC>(x[u].v[j], y[j]);
 #pragma unroll
-        for (int i = 0; i < NT; ++i) multiply(i, exchange(q[u][i]), s_now[i].v[u], y);
+        for (int i = 0; i < NT; ++i) multiply(i, exchange(permuted(q[u][i], from)), permuted(s_now[i], ((lane & 15) * 4 + u) * 4), y);
       }
       __builtin_amdgcn_sched_barrier(0);
       if constexpr (decltype(next)::value) {
@@ -133,17 +135,20 @@ __global__ __launch_bounds__(64 * kMaxWaves) void group_rows(const typename Elem
   }
   // what no run takes: the columns past the last whole block, or few blocks
   for (int k = full + wave; k * 4 < groups; k += waves) {
-    const int g = min(k * 4 + part, groups - 1);
+    const int g = min(k * 4 + in_quad, groups - 1);
     bf16x8 y[4][kParts];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) load_parts<SRC>(pa, k * kBlockCols + j * kGroup + part * 8, cols, y[j]);
+    for (int j = 0; j < 4; ++j) {
+      load_parts<SRC>(pa, k * kBlockCols + j * kGroup + part * 8, cols, y[j]);
+    }
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       uint32_t scales = 0;  // of groups that there are not, one that is finite
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (k * 4 + j < groups) scales |= uint32_t(sb[i][k * 4 + j]) << (8 * j);
-      multiply(i, exchange(*reinterpret_cast<const i32x4*>(pb[i] + int64_t(g) * 16)), scales, y);
+      multiply(i, exchange(permuted(*reinterpret_cast<const i32x4*>(pb[i] + int64_t(g) * 16), from)),
+               permuted(scales, (lane & 15) * 16), y);
     }
   }
 #pragma unroll
@@ -174,8 +179,10 @@ hipError_t product_as(const GroupPlan& plan, const reshard_matrix_t& a, const re
   switch (plan.n_tiles) {
     case 1: return rows_as<SRC, DT, 1>(plan, a, b, offsets, experts, out, stream);
     case 2: return rows_as<SRC, DT, 2>(plan, a, b, offsets, experts, out, stream);
-    default: return rows_as<SRC, DT, 4>(plan, a, b, offsets, experts, out, stream);
+    default:
+      if constexpr (Parts<SRC>::count == 1) return rows_as<SRC, DT, 4>(plan, a, b, offsets, experts, out, stream);
   }
+  return hipErrorInvalidValue;
 }
 
 template <int SRC>
@@ -190,12 +197,6 @@ hipError_t product_from(const GroupPlan& plan, const reshard_matrix_t& a, const 
 
 }  // namespace
 
-#ifndef SPLC
-#define SPLC 2
-#endif
-#ifndef SPLS
-#define SPLS 6
-#endif
 GroupPlan plan_group_matmul(const reshard_matrix_t& a, const reshard_matrix_t& b, int64_t experts,
                             const reshard_matrix_t& out) {
   GroupPlan p;
@@ -214,9 +215,14 @@ GroupPlan plan_group_matmul(const reshard_matrix_t& a, const reshard_matrix_t& b
   const int64_t stride = std::max(direct ? a.row_stride * 2 : parts * part_steps * 128, std::max(b.row_stride / 2, b.scale_stride));
   // (their rows are at most 2^22 bytes apart, a tile's within 32-bit offsets, and they load
   // eight scales of a row together)
+  // Which form, by the rows of a weight (us): up to 16, 16 x 14336 x 4096 11.4 with the form
+  // for few rows and 13.9 with tiles of 64; up to 64, 33 x 14336 x 4096 18.3 with those.  Larger
+  // tiles where they fill the card: 512 x 14336 x 4096 63 with 128 x 128, 73 with 64 x 128; 64
+  // experts' 9600 rows 417 and 450, their 4800 294 and 290; 4096 x 14336 x 4096 440 with 256 x
+  // 256, 64 experts' 16384 rows 603 and 645 with 128 x 128, their 4800 393 and 294.
   const int64_t mean = experts ? a.rows / experts : a.rows;
   if (mean > kRowsHeight && groups_of(a.cols) >= 8 && out.cols && stride <= (int64_t(1) << 22)) {
-    if (tiles(256, 256) >= 192 && (!experts || mean >= 192)) {
+    if (tiles(256, 256) >= 192 && out.cols > 128 && (!experts || mean >= 192)) {
       p.form = GroupPlan::kTiles256;
       p.whole = experts ? 0 : whole_tiles(tiles(256, 256));
       p.groups = experts ? tiles(256, 256) : 2 * tiles(256, 256) - p.whole;
@@ -232,8 +238,10 @@ GroupPlan plan_group_matmul(const reshard_matrix_t& a, const reshard_matrix_t& b
     p.steps_per_split = p.steps;
     if (!direct) p.planes = round_up(a.rows * parts * part_steps * 128, 256);
     if (p.form == GroupPlan::kTiles64 && !experts) {
+      // a workgroup a CU shares the contractions, six steps at least each (128 x 14336 x 4096
+      // 25 us, with two a CU 28)
       const int64_t t = p.groups;
-      int64_t splits = std::max<int64_t>(1, std::min(SPLC * kCus / t, ceil_div(p.steps, SPLS)));
+      const int64_t splits = std::max<int64_t>(1, std::min(kCus / t, ceil_div(p.steps, 6)));
       p.steps_per_split = uint32_t(ceil_div(ceil_div(p.steps, splits), 3) * 3);
       p.splits = int(ceil_div(p.steps, p.steps_per_split));
       p.whole = p.groups = t * p.splits;
@@ -241,20 +249,15 @@ GroupPlan plan_group_matmul(const reshard_matrix_t& a, const reshard_matrix_t& b
     }
     return p;
   }
-  const int64_t runs = std::max<int64_t>(1, ceil_div(a.cols / (4 * kGroup), kRun));
-#ifndef NTMIN
-#define NTMIN 448
-#endif
-#ifndef NTMAX
-#define NTMAX 4
-#endif
+  // As many columns a workgroup as leave 200 of them: what a costs is a workgroup's reading
+  // of all of it (16 x 14336 x 4096 11.4 us with 64 columns, 14.4 with 32).  Elements in
+  // parts have registers for 32.
+  const int most = parts == 1 ? 4 : 2;
   p.n_tiles = 1;
-  while (p.n_tiles < NTMAX && tiles(kRowsHeight, 32 * p.n_tiles) >= NTMIN) p.n_tiles *= 2;
+  while (p.n_tiles < most && tiles(kRowsHeight, 32 * p.n_tiles) >= 200) p.n_tiles *= 2;
   p.groups = tiles(kRowsHeight, 16 * p.n_tiles);
-#ifndef MAXW
-#define MAXW 16
-#endif
-  p.waves = int(ceil_div(runs, ceil_div(runs, MAXW)));
+  const int64_t runs = std::max<int64_t>(1, ceil_div(a.cols / kBlockCols, kRun));
+  p.waves = int(ceil_div(runs, ceil_div(runs, kMaxWaves)));
   return p;
 }
 

@@ -29,12 +29,20 @@ constexpr int kRowA = kStep * 2, kRowB = kThree * kStep / 2;  // bytes of a row 
 // 14336 x 4096).  A lane (row, quarter q) reads 16 consecutive columns of its row on both
 // sides, 8 for each of two instructions, and widens the weight's to bfloat16, scaled, in
 // registers: one scale of the row's two.  The scales of three steps (6 bytes a row) are
-// loaded into registers a step ahead, as they lie: a shift there would wait for them.
-template <int DT, int BM, int BN, int WM, int WN>
+// loaded into registers, as they lie: a shift there would wait for them.  SHARED: by one
+// thread a row and through LDS (512 x 14336 x 4096 72 -> 63 us; neighbouring lanes that each
+// read another row cost the first cache a line each).  In tiles of 256 rows, whose registers
+// are full, by every lane that uses them.
+//
+// 256 x 256 tiles: 4096 x 14336 x 4096 takes 440 us (1090 TFLOP/s; the library's product of
+// bfloat16 matrices 406), with an MFMA pipe that is busy for 45% of the time; without the
+// loads it would take 382, without the conversions 435.  128 x 128, two workgroups a CU:
+// 512 x 14336 x 4096 63 us.  64 x 128: 33 x 4096 x 14336 14 us and 4 for the join.
+template <int DT, int BM, int BN, int WM, int WN, bool SHARED>
 __device__ __forceinline__ void make_tile(const Rows& a, const Weight& b, int groups, const Chunk& c, int n0,
                                           uint32_t first, uint32_t last, uint32_t part_steps,
                                           typename Elem<DT>::type* out, int64_t out_stride, uint8_t* a0, uint8_t* a1,
-                                          uint8_t* a2, uint8_t* b0, uint8_t* b1) {
+                                          uint8_t* a2, uint8_t* b0, uint8_t* b1, uint64_t* row_scales) {
   constexpr int kThreads = 64 * WM * WN, kM = BM / WM / 16, kN = BN / WN / 16;
   constexpr int kLoadsA = BM * 8 / kThreads, kLoadsB = BN * 6 / kThreads;
   static_assert(kM > 2 && kThreads % 128 == 0 && BN * 6 % kThreads == 0 && BM * 8 % kThreads == 0, "");
@@ -71,19 +79,32 @@ __device__ __forceinline__ void make_tile(const Rows& a, const Weight& b, int gr
       load_to_lds(base_b, to + (i * kThreads + wave * 64) * 16, off_b[i], min(kb, last_b) * (kStep / 2));
   };
 
-  const uint8_t* scales = b.scales + row_b0 * b.scale_stride;
-  uint32_t off_s[kN];
-#pragma unroll
-  for (int i = 0; i < kN; ++i)
-    off_s[i] = uint32_t(min(wn * (BN / WN) + i * 16 + frow, n_rows - 1)) * uint32_t(b.scale_stride);
-  // Eight scale bytes of a row for the weight's steps kb to kb + 2, whose first is at bit
+  // Eight scale bytes of a row of the weight for its steps kb to kb + 2, whose first is at bit
   // scales_at(kb): the row's last eight at most.  Past the last group any of the row's
   // does: a is zero there.
+  const uint8_t* scales = b.scales + row_b0 * b.scale_stride;
   const auto scales_at = [&](uint32_t kb) { return 8 * (int(kb) * 2 - min(int(kb) * 2, groups - 8)); };
-  const auto load_scales = [&](uint64_t (&s)[kN], uint32_t kb) {
-    const int at = min(int(kb) * 2, groups - 8);
+  constexpr int kScaleRows = SHARED ? 1 : kN;
+  uint32_t off_s[kScaleRows];
 #pragma unroll
-    for (int i = 0; i < kN; ++i) __builtin_memcpy(&s[i], scales + (off_s[i] + uint32_t(at)), 8);
+  for (int i = 0; i < kScaleRows; ++i)
+    off_s[i] = uint32_t(min(SHARED ? int(threadIdx.x) : wn * (BN / WN) + i * 16 + frow, n_rows - 1)) * uint32_t(b.scale_stride);
+  uint64_t loaded[kScaleRows];
+  const auto load_scales = [&](uint32_t kb) {
+    if (!SHARED || threadIdx.x < BN) {
+#pragma unroll
+      for (int i = 0; i < kScaleRows; ++i)
+        __builtin_memcpy(&loaded[i], scales + (off_s[i] + uint32_t(min(int(kb) * 2, groups - 8))), 8);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  const auto share_scales = [&] {
+    if (SHARED && threadIdx.x < BN) row_scales[threadIdx.x] = loaded[0];
+  };
+  uint64_t s[kN];
+  const auto take_scales = [&] {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) s[i] = SHARED ? row_scales[wn * (BN / WN) + i * 16 + frow] : loaded[i % kScaleRows];
   };
 
   f32x4 acc[kN][kM];
@@ -153,19 +174,20 @@ __device__ __forceinline__ void make_tile(const Rows& a, const Weight& b, int gr
   // and, while they are young, the weight's next three.  (Scales come on top of them: a
   // barrier that waits for more than it has to is no fault.)
   uint32_t kb = first % part_steps, k = first;
-  uint64_t s[kN];
-  load_scales(s, kb);
-  __builtin_amdgcn_sched_barrier(0);
+  load_scales(kb);
   load_b(b0, kb);
   load_a(a0, first);
   load_a(a1, min(first + 1, last - 1));
+  share_scales();
   loads_barrier<kLoadsA>();
+  take_scales();
   begin(a0, b0, 0);
   uint32_t kn;  // the weight's next three: it starts over for a's next part
   int bit;
   const auto first_of = [&](const uint8_t* now, uint8_t* later) {
     kn = kb + 3 < part_steps ? kb + 3 : 0;
     bit = scales_at(kb);
+    if constexpr (SHARED) load_scales(kn);
     step(a0, s, bit, [&] { load_a(a2, min(k + 2, last - 1)); load_b(later, kn); }, [&] {
       loads_barrier<kLoadsA + kLoadsB>();  // a1 has arrived, a0 has been read
       begin(a1, now, 1);
@@ -173,17 +195,18 @@ __device__ __forceinline__ void make_tile(const Rows& a, const Weight& b, int gr
   };
   const auto second_of = [&](const uint8_t* now) {
     step(a1, s, bit + 16, [&] { load_a(a0, min(k + 3, last - 1)); }, [&] {
+      share_scales();  // those before were taken before the last barrier
       loads_barrier<kLoadsA + kLoadsB>();
       begin(a2, now, 2);
     });
   };
   const auto third_of = [&](const uint8_t* later) {
     step(a2, s, bit + 32, [&] {
-      load_scales(s, kn);  // this step's are in use already
-      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (!SHARED) load_scales(kn);
       load_a(a1, min(k + 4, last - 1));
     }, [&] {
       loads_barrier<kLoadsA>();  // the next three steps' weight too
+      take_scales();             // this step's are in use already
       begin(a0, later, 0);
     });
     kb = kn;
@@ -237,6 +260,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void group_tiles(Rows a, Weight b,
   __shared__ __align__(128) uint8_t a2[BM * kRowA];
   __shared__ __align__(128) uint8_t b0[BN * kRowB];
   __shared__ __align__(128) uint8_t b1[BN * kRowB];
+  constexpr bool kShared = BM < 256;
+  __shared__ uint64_t row_scales[kShared ? BN : 1];
   Chunk c;
   uint32_t n_tile, split = 0;
   if (offsets) {
@@ -263,11 +288,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void group_tiles(Rows a, Weight b,
   }
   const uint32_t first = split * steps_per_split, last = min(first + steps_per_split, steps);
   if (BM == 256 && c.last - c.first <= BM / 2)
-    make_tile<DT, BM == 256 ? 128 : BM, BN, WM, WN>(a, b, groups, c, int(n_tile) * BN, first, last, part_steps,
-                                                    out + split * split_stride, out_stride, a0, a1, a2, b0, b1);
+    make_tile<DT, BM == 256 ? 128 : BM, BN, WM, WN, kShared>(a, b, groups, c, int(n_tile) * BN, first, last, part_steps,
+                                                    out + split * split_stride, out_stride, a0, a1, a2, b0, b1, row_scales);
   else
-    make_tile<DT, BM, BN, WM, WN>(a, b, groups, c, int(n_tile) * BN, first, last, part_steps, out + split * split_stride,
-                                  out_stride, a0, a1, a2, b0, b1);
+    make_tile<DT, BM, BN, WM, WN, kShared>(a, b, groups, c, int(n_tile) * BN, first, last, part_steps, out + split * split_stride,
+                                  out_stride, a0, a1, a2, b0, b1, row_scales);
 }
 
 // The bfloat16 parts of a's rows, one behind the other, each of `width` columns, zero past
