@@ -1,17 +1,20 @@
-"""Refit of trained weights to an 8-bit inference layout.
+"""Refit of trained weights to an 8-bit or a 4-bit inference layout.
 
 The pages mention that the refit supports precision modes and say nothing more
 (the news.bpdata.com and techfeed.io write-ups, closing remarks on the refit
 guide).  The reading taken here: the trainer holds fp32, bf16 or fp16 weights,
 the inference engine 8-bit ones with a power-of-two scale for each block of
-128 x 128 (the block-scaled format of ``include/reshard.h``).  Every source shard
-is quantized where it lies and one reshard then moves payload and scales, so
-that the move carries one byte an element instead of two or four, and every
-destination replica receives the same bytes.
+128 x 128 (the block-scaled format of ``include/reshard.h``), or 4-bit ones with
+one for each group of 32 columns (the group-scaled format), experts stacked in
+front among them.  Every source shard is quantized where it lies and one reshard
+then moves payload and scales, so that the move carries one byte an element, or
+half of one, instead of two or four, and every destination replica receives the
+same bytes.
 
-Blocks must not be cut: every shard's runs start at a multiple of 128 and end at
-one or at the tensor's edge, on both sides; other layouts are refused.  The
-result is then that of quantizing the whole tensor.
+Blocks must not be cut: every shard's runs start at a multiple of 128 (of 32 along
+the columns of a 4-bit weight, whose rows may be cut anywhere) and end at one or
+at the tensor's edge, on both sides; other layouts are refused.  The result is
+then that of quantizing the whole tensor.
 """
 from __future__ import annotations
 
@@ -20,12 +23,13 @@ from . import reshard as R
 FLOATS = (R.DTYPE_F32, R.DTYPE_BF16, R.DTYPE_F16)
 
 
-def _blocks(n: int) -> int:
-    return -(-n // R.BLOCK)
+def _blocks(n: int, block: int = R.BLOCK) -> int:
+    return -(-n // block)
 
 
 class QuantizedPlan:
-    """Plan for a list of 2-d weights (objects with name, shape, dtype, src_mesh,
+    """Plan for a list of 2-d weights, with ``DTYPE_FP4_E2M1`` of 3-d stacks of experts'
+    too (objects with name, shape, dtype, src_mesh,
     src_placements, dst_mesh, dst_placements and optionally src_split / dst_split,
     e.g. workloads.TensorSpec; out_dtype is not looked at).
 
@@ -33,12 +37,17 @@ class QuantizedPlan:
     shards (contiguous, the spec's dtype), a payload and a scale buffer for each
     source rank, and a payload and a scale buffer for each destination rank, of
     ``payload_shapes`` and ``scale_shapes`` (one byte an element, contiguous;
-    payload columns are rounded up to whole blocks).
+    payload columns are rounded up to whole blocks).  In 4 bits a shard of a stack is
+    one matrix, its experts' rows one below the other, and its payload's columns count
+    bytes of two elements.
     """
 
     def __init__(self, specs, dtype: int = R.DTYPE_FP8_E4M3):
         self.specs = list(specs)
         self.dtype = dtype
+        # columns and rows of a block, columns of a block's payload in bytes
+        self._cols, self._rows, self._bytes = (
+            (R.GROUP, 1, R.GROUP // 2) if dtype == R.DTYPE_FP4_E2M1 else (R.BLOCK, R.BLOCK, R.BLOCK))
         self.plan = None
         self._layouts = []
         try:
@@ -55,29 +64,34 @@ class QuantizedPlan:
     def _build(self):
         if not self.specs:
             raise ValueError("need at least one tensor")
-        if self.dtype not in (R.DTYPE_FP8_E4M3, R.DTYPE_FP8_E5M2):
-            raise ValueError("dtype is not FP8_E4M3 or FP8_E5M2")
+        if self.dtype not in (R.DTYPE_FP8_E4M3, R.DTYPE_FP8_E5M2, R.DTYPE_FP4_E2M1):
+            raise ValueError("dtype is not FP8_E4M3, FP8_E5M2 or FP4_E2M1")
+        stacks = self.dtype == R.DTYPE_FP4_E2M1
         payload, scales = {"src": [], "dst": []}, {"src": [], "dst": []}
         self._shapes = {"src": [], "dst": []}  # per tensor, per rank: (rows, cols) of the shard
         for spec in self.specs:
-            if len(spec.shape) != 2:
-                raise ValueError(f"{spec.name}: only 2-d weights are quantized")
+            if len(spec.shape) != 2 and not (stacks and len(spec.shape) == 3):
+                raise ValueError(f"{spec.name}: only 2-d weights are quantized" + (", and 3-d stacks" if stacks else ""))
             if R.dtype_code(spec.dtype) not in FLOATS:
                 raise ValueError(f"{spec.name}: dtype is not F32, BF16 or F16")
             if R.PARTIAL in tuple(spec.src_placements):
                 raise ValueError(f"{spec.name}: Partial contributions cannot be quantized before they are added")
-            n, k = spec.shape
-            grid = (_blocks(n), _blocks(k))
+            *lead, n, k = spec.shape
+            grid = (*lead, _blocks(n, self._rows), _blocks(k, self._cols))
             for side in ("src", "dst"):
                 mesh, pl = getattr(spec, side + "_mesh"), getattr(spec, side + "_placements")
                 split = getattr(spec, side + "_split", None)
-                whole = self._layout((n, k), R.dtype_code(spec.dtype), mesh, pl, split)
-                held = self._layout((n, grid[1] * R.BLOCK), self.dtype, mesh, pl, split)
+                whole = self._layout(spec.shape, R.dtype_code(spec.dtype), mesh, pl, split)
+                held = self._layout((*lead, n, grid[-1] * self._bytes), R.DTYPE_U8 if stacks else self.dtype, mesh, pl,
+                                    split)
                 scale = self._layout(grid, R.DTYPE_U8, mesh, pl, split)
                 shapes = []
                 for rank in range(R.reshard_layout_num_ranks(whole)):
                     self._check_cuts(spec, side, rank, whole, held, scale)
-                    shapes.append(tuple(R.local_shape(whole, rank, 2)))
+                    *outer, rows, cols = R.local_shape(whole, rank, len(spec.shape))
+                    for m in outer:
+                        rows *= m
+                    shapes.append((rows, cols))
                 self._shapes[side].append(shapes)
                 payload[side].append(held)
                 scales[side].append(scale)
@@ -94,15 +108,18 @@ class QuantizedPlan:
             at += len(shapes)
 
     def _check_cuts(self, spec, side, rank, whole, held, scale):
+        last = len(spec.shape) - 1
         for dim, extent in enumerate(spec.shape):
+            block = self._cols if dim == last else self._rows if dim == last - 1 else 1
             runs = R.reshard_layout_shard_runs(whole, rank, dim)
             for lo, hi in runs:
-                if lo % R.BLOCK or (hi % R.BLOCK and hi != extent):
+                if lo % block or (hi % block and hi != extent):
                     raise ValueError(f"{spec.name}: {side} rank {rank} cuts dim {dim} at [{lo}, {hi}), inside a "
-                                     f"block of {R.BLOCK}")
-            end = lambda hi: _blocks(hi) * R.BLOCK if dim == 1 else hi
-            if (R.reshard_layout_shard_runs(held, rank, dim) != [(lo, end(hi)) for lo, hi in runs] or
-                    R.reshard_layout_shard_runs(scale, rank, dim) != [(lo // R.BLOCK, _blocks(hi)) for lo, hi in runs]):
+                                     f"block of {block}")
+            blocks = [(lo // block, _blocks(hi, block)) for lo, hi in runs]
+            payload = [(lo * self._bytes, hi * self._bytes) for lo, hi in blocks] if dim == last else runs
+            if (R.reshard_layout_shard_runs(held, rank, dim) != payload or
+                    R.reshard_layout_shard_runs(scale, rank, dim) != blocks):
                 raise ValueError(f"{spec.name}: {side} rank {rank} splits dim {dim} and its blocks differently")
 
     # ------------------------------------------------------------- buffers
@@ -112,15 +129,17 @@ class QuantizedPlan:
         return list(self._shapes[side][t])
 
     def payload_shapes(self, t: int, side: str):
-        return [(r, _blocks(c) * R.BLOCK) for r, c in self._shapes[side][t]]
+        """(rows, bytes of a row) of each rank's payload."""
+        return [(r, _blocks(c, self._cols) * self._bytes) for r, c in self._shapes[side][t]]
 
     def scale_shapes(self, t: int, side: str):
-        return [(_blocks(r), _blocks(c)) for r, c in self._shapes[side][t]]
+        return [(_blocks(r, self._rows), _blocks(c, self._cols)) for r, c in self._shapes[side][t]]
 
     def weight(self, t: int, rank: int, payload: int, scales: int, side: str = "dst") -> R.Matrix:
-        """The block-scaled matrix of a rank's shard, as the products take it."""
+        """The block- or group-scaled matrix of a rank's shard, as the products take it."""
         r, c = self._shapes[side][t][rank]
-        return R.matrix(r, c, self.dtype, payload, _blocks(c) * R.BLOCK, R.BLOCK, scales, _blocks(c))
+        blocks = _blocks(c, self._cols)
+        return R.matrix(r, c, self.dtype, payload, blocks * self._cols, self._rows, scales, blocks)
 
     def bind(self, src, src_payload, src_scales, dst_payload, dst_scales):
         """Handles for ``execute``, reusable as long as the buffers live.  Each
@@ -146,7 +165,8 @@ class QuantizedPlan:
             size = R.reshard_dtype_size(R.dtype_code(spec.dtype))
             for read, (r, c) in zip(self._read[t], self._shapes["src"][t]):
                 if read:
-                    total += r * c * size + r * _blocks(c) * R.BLOCK + _blocks(r) * _blocks(c)
+                    blocks = _blocks(c, self._cols)
+                    total += r * c * size + r * blocks * self._bytes + _blocks(r, self._rows) * blocks
         return total
 
     def execute(self, bound, stream: int):
@@ -154,7 +174,10 @@ class QuantizedPlan:
         all on one stream (a raw hipStream_t address; 0 = the null stream)."""
         jobs, src, dst = bound
         for plain, held in jobs:
-            R.reshard_block_quantize(plain, held, None, stream)
+            if self.dtype == R.DTYPE_FP4_E2M1:
+                R.reshard_group_quantize(plain, held, stream)
+            else:
+                R.reshard_block_quantize(plain, held, None, stream)
         R.reshard_execute(self.plan, src, dst, stream)
 
     def close(self):

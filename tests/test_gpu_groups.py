@@ -17,6 +17,8 @@ import torch
 import dtensor_layout_movement_amd as R
 import group_reference as ref
 from group_reference import GROUP
+from dtensor_layout_movement_amd import workloads as W
+from dtensor_layout_movement_amd.quantized import QuantizedPlan
 from test_gpu_blocks import CANARY, DTYPES, Plain, stream, workspace
 
 pytestmark = pytest.mark.gpu
@@ -344,3 +346,129 @@ def test_quantizing_into_columns_of_one_buffer():
     for at in (0, 1):
         assert np.array_equal(ref.values(pay[:, 64 * at:64 * at + 48], sc[:, 4 * at:4 * at + 3], rows, cols), want)
     assert bool((pay[:, 48:64] == CANARY).all()) and bool((sc[:, 3] == CANARY).all())
+
+
+# --------------------------------------------------------------- refit to 4 bits
+
+T, RR = W.TensorSpec, W.R
+LISTS = {
+    "rows cut anywhere to columns": [T("w", (301, 512), torch.bfloat16, (4,), (0,), (2,), (1,))],
+    "columns with an edge, replicas": [T("w", (130, 511), torch.float32, (2,), (1,), (2, 3), (RR, 0))],
+    "a stack of experts": [T("e", (6, 40, 96), torch.float16, (3, 2), (0, 1), (2, 3), (0, 2))],
+    "several": [T("a", (33, 70), torch.float32, (1,), (0,), (1,), (0,)), T("b", (4, 5, 64), torch.bfloat16, (4,), (0,), (2,), (2,))],
+}
+
+
+@pytest.mark.parametrize("name", list(LISTS))
+def test_every_destination_rank_holds_its_part_of_the_quantized_whole(name):
+    specs = LISTS[name]
+
+    def parts(spec, side):
+        h = R.layout_create(spec.shape, R.dtype_code(spec.dtype), getattr(spec, side + "_mesh"), getattr(spec, side + "_placements"))
+        try:
+            return [tuple(slice(*R.reshard_layout_shard_runs(h, r, d)[0]) for d in range(len(spec.shape)))
+                    for r in range(R.reshard_layout_num_ranks(h))]
+        finally:
+            R.reshard_layout_destroy(h)
+
+    whole = [values_of((int(np.prod(s.shape[:-1])), s.shape[-1]), "normal" if s.dtype != torch.float32 else "special", t, s.dtype)
+             .view(s.shape) for t, s in enumerate(specs)]
+    src = [[w[box].contiguous().cuda() for box in parts(s, "src")] for s, w in zip(specs, whole)]
+    plan = QuantizedPlan(specs, R.DTYPE_FP4_E2M1)
+    try:
+        bufs = {(side, what): [[torch.full((max(1, r * c),), CANARY, dtype=torch.uint8, device="cuda")
+                                for r, c in getattr(plan, what + "_shapes")(t, side)] for t in range(len(specs))]
+                for side in ("src", "dst") for what in ("payload", "scale")}
+        ptrs = {k: [[b.data_ptr() for b in per] for per in v] for k, v in bufs.items()}
+        bound = plan.bind([[s.data_ptr() for s in per] for per in src], ptrs["src", "payload"], ptrs["src", "scale"],
+                          ptrs["dst", "payload"], ptrs["dst", "scale"])
+        plan.execute(bound, stream())
+        torch.cuda.synchronize()
+        for t, (s, w) in enumerate(zip(specs, whole)):
+            want, scales = ref.quantize(w.reshape(-1, s.shape[-1]))
+            want, scales = want.reshape(s.shape), scales.reshape(*s.shape[:-1], -1)
+            for rank, box in enumerate(parts(s, "dst")):
+                part = want[box].reshape(-1, want[box].shape[-1])
+                rows, cols = plan.shard_shapes(t, "dst")[rank]
+                assert part.shape == (rows, cols)
+                q = bufs["dst", "payload"][t][rank].view(plan.payload_shapes(t, "dst")[rank])
+                sc = bufs["dst", "scale"][t][rank].view(plan.scale_shapes(t, "dst")[rank])
+                assert np.array_equal(ref.values(q, sc, rows, cols), part, equal_nan=True), (t, rank)
+                groups = slice(box[-1].start // GROUP, -(-box[-1].stop // GROUP))
+                assert np.array_equal(sc.cpu().numpy(), scales[(*box[:-1], groups)].reshape(rows, -1))
+    finally:
+        plan.close()
+
+
+# ---------------------------------------------- every form, by the shapes that take it
+
+
+@pytest.mark.parametrize("src", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("m,n,k", [(16, 3300, 2100), (16, 13000, 640), (64, 300, 6000), (70, 260, 20000), (65, 33000, 256),
+                                   (257, 50000, 232), (2000, 6400, 320)])
+def test_forms_of_the_products(m, n, k, src):
+    """Few rows with 16 to 64 columns a workgroup, tiles of 64 with shared contractions, of
+    128, of 256 with half tiles; checked on rows and columns drawn from all of it."""
+    g = torch.Generator().manual_seed(m + n)
+    a = Plain(m, k, DTYPES[src], value=torch.randn(m, k, generator=g).to(DTYPES[src]))
+    b, o = Grouped(n, k).fill(n, 120, 128), Plain(m, n, torch.float32)
+    keep, args = room(R.reshard_group_matmul_workspace(a.m, b.m, o.m))
+    R.reshard_group_matmul(a.m, b.m, o.m, *args, stream())
+    torch.cuda.synchronize()
+    rows = torch.unique(torch.cat([torch.arange(min(m, 3)), torch.arange(max(0, m - 3), m), torch.randint(0, m, (60,), generator=g)]))
+    cols = torch.unique(torch.cat([torch.arange(min(n, 40)), torch.arange(max(0, n - 40), n), torch.randint(0, n, (400,), generator=g)]))
+    av = a.view.cpu()[rows].double().numpy()
+    bv = ref.values(b.payload.cpu()[cols][:, :b.width], b.scales.cpu()[cols][:, :b.groups], len(cols), k)
+    check(o.view.cpu()[rows][:, cols], av @ bv.T, np.abs(av) @ np.abs(bv).T, k * PARTS[src] + 1, "f32", (m, n, k))
+    assert bool(torch.isfinite(o.view).all())
+    o.check_rest()
+    # the same call in a graph, replayed with eager work between
+    want = o.view.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        R.reshard_group_matmul(a.m, b.m, o.m, *args, stream())
+    for _ in range(2):
+        o.view.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o.view, want)
+
+
+def test_rows_far_apart_take_the_form_that_has_no_limit():
+    """More than 2^22 bytes from row to row of the payload (here of one row more than
+    fits): many rows of a go sixteen at a time."""
+    m, n, k = 40, 3, 256
+    stride = (1 << 23) + 64  # elements
+    pay = torch.full((3 * stride // 2,), CANARY, dtype=torch.uint8, device="cuda")
+    sc = torch.full((n, 8), 127, dtype=torch.uint8, device="cuda")
+    small = Grouped(n, k).fill(9, 127, 128)
+    for r in range(n):
+        pay[r * stride // 2:r * stride // 2 + k // 2] = small.payload[r, :k // 2]
+    a = Plain(m, k, torch.bfloat16, value=torch.randn(m, k, generator=torch.Generator().manual_seed(1)).bfloat16())
+    o, want = Plain(m, n, torch.float32), Plain(m, n, torch.float32)
+    b = R.matrix(n, k, R.DTYPE_FP4_E2M1, pay.data_ptr(), stride, 1, sc.data_ptr(), 8)
+    keep, args = room(R.reshard_group_matmul_workspace(a.m, b, o.m))
+    R.reshard_group_matmul(a.m, b, o.m, *args, stream())
+    torch.cuda.synchronize()
+    av, bv = a.view.cpu().double().numpy(), small.values()
+    check(o.view, av @ bv.T, np.abs(av) @ np.abs(bv).T, k + 1, "f32")
+
+
+def test_weights_past_four_gigabytes():
+    """A payload whose last rows lie past 2^32 bytes, in both kinds of forms."""
+    n, k = 300000, 32768
+    pay = torch.zeros(n, k // 2, dtype=torch.uint8, device="cuda")
+    sc = torch.full((n, k // 32), 127, dtype=torch.uint8, device="cuda")
+    assert pay.numel() > 1 << 32
+    last = Grouped(64, k).fill(4, 127, 128)
+    pay[n - 64:] = last.payload[:64, :k // 2]
+    b = R.matrix(n, k, R.DTYPE_FP4_E2M1, pay.data_ptr(), k, 1, sc.data_ptr(), k // 32)
+    for m in (2, 300):
+        a = Plain(m, k, torch.bfloat16, value=torch.randn(m, k, generator=torch.Generator().manual_seed(m)).bfloat16())
+        o = Plain(m, n, torch.bfloat16)
+        keep, args = room(R.reshard_group_matmul_workspace(a.m, b, o.m))
+        R.reshard_group_matmul(a.m, b, o.m, *args, stream())
+        torch.cuda.synchronize()
+        av, bv = a.view.cpu().double().numpy(), last.values()
+        check(o.view[:, n - 64:], av @ bv.T, np.abs(av) @ np.abs(bv).T, k + 1, "bf16")
+        assert bool((o.view[:, :n - 64] == 0).all())

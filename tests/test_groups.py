@@ -259,3 +259,49 @@ def test_reference_sorts_in_order():
     offsets, position = ref.sort(ids, 1, 3)
     assert list(offsets) == [0, 3, 3, 6]
     assert position.tolist() == [[3, 0], [1, -1], [-1, 4], [2, 5]]
+
+
+# ------------------------------------------------------------- refit to 4 bits
+
+from dtensor_layout_movement_amd import workloads as WL  # noqa: E402
+from dtensor_layout_movement_amd.quantized import QuantizedPlan  # noqa: E402
+
+T, BF, RR = WL.TensorSpec, torch.bfloat16, WL.R
+
+
+def test_four_bit_plan_shapes():
+    p = QuantizedPlan([T("up", (1000, 511), BF, (3,), (0,), (2, 2), (RR, 1)),
+                       T("experts", (8, 40, 96), torch.float32, (4, 2), (0, 1), (2, 3), (0, 2))], R.DTYPE_FP4_E2M1)
+    try:
+        assert p.shard_shapes(0, "src") == [(334, 511), (334, 511), (332, 511)]  # rows are cut anywhere
+        assert p.payload_shapes(0, "dst") == [(1000, 128)] * 4 and p.scale_shapes(0, "dst") == [(1000, 8)] * 4
+        assert p.shard_shapes(0, "dst") == [(1000, 256), (1000, 255)] * 2
+        assert p.shard_shapes(1, "src") == [(40, 96)] * 8 and p.shard_shapes(1, "dst") == [(160, 32)] * 6
+        assert p.payload_shapes(1, "dst") == [(160, 16)] * 6 and p.scale_shapes(1, "dst") == [(160, 1)] * 6
+        m = p.weight(1, 0, P, 2 * P)
+        assert (m.rows, m.cols, m.dtype, m.block_rows, m.row_stride, m.scale_stride) == (160, 32, I4, 1, 32, 1)
+        st = R.reshard_plan_stats(p.plan)
+        assert st["bytes_written"] == 2 * 1000 * (256 + 16) + 8 * 40 * (48 + 3)
+    finally:
+        p.close()
+
+
+@pytest.mark.parametrize("spec,text", [
+    (T("c", (256, 300), BF, (1,), (0,), (2,), (1,)), "inside a block of 32"),
+    (T("s", (2, 2, 64, 64), BF, (1,), (0,), (1,), (0,)), "2-d weights are quantized, and 3-d"),
+    (T("p", (256, 256), BF, (2,), (WL.P,), (1,), (0,)), "Partial"),
+    (T("i", (256, 256), torch.int32, (1,), (0,), (1,), (0,)), "dtype"),
+])
+def test_four_bit_plan_refusals(spec, text):
+    with pytest.raises(ValueError, match=text):
+        QuantizedPlan([spec], R.DTYPE_FP4_E2M1)
+
+
+@pytest.mark.parametrize("wl", [WL.ffn_up(), WL.ffn_refit(4), WL.moe_experts()], ids=lambda w: w.name)
+def test_four_bit_plan_takes_the_workloads(wl):
+    p = QuantizedPlan(wl.tensors, R.DTYPE_FP4_E2M1)
+    try:
+        direct = sum(2 * int(np.prod(spec.shape)) for spec in wl.tensors)
+        assert R.reshard_plan_stats(p.plan)["bytes_read"] == direct // 4 + direct // 64
+    finally:
+        p.close()
