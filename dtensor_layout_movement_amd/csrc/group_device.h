@@ -53,17 +53,20 @@ __device__ __forceinline__ bool find_tile(const int32_t* offsets, int experts, i
   const uint32_t t = run_of(id, uint32_t(total) * n_tiles);
   int slot = int(t / n_tiles);
   *n_tile = t % n_tiles;
-  for (int base = 0;; base += 64) {
+  // (bounded, and cut to the expert's rows: offsets that overlap may count more chunks
+  // than an integer holds)
+  for (int base = 0; base < experts; base += 64) {
     if (base) of = count_chunks(offsets, experts, rows, height, base);
     const uint64_t past = __ballot(of.upto > slot);
     if (past) {
-      const int l = __builtin_ctzll(past);
-      const int first = __builtin_amdgcn_readlane(of.lo, l) + (slot - __builtin_amdgcn_readlane(of.upto - of.n, l)) * height;
-      *c = Chunk{base + l, first, min(first + height, __builtin_amdgcn_readlane(of.hi, l))};
-      return true;
+      const int l = __builtin_ctzll(past), lo = __builtin_amdgcn_readlane(of.lo, l), hi = __builtin_amdgcn_readlane(of.hi, l);
+      const int first = lo + (slot - __builtin_amdgcn_readlane(of.upto - of.n, l)) * height;
+      *c = Chunk{base + l, first, min(first + height, hi)};
+      return first >= lo && first < hi;
     }
     slot -= __builtin_amdgcn_readlane(of.upto, 63);
   }
+  return false;
 }
 
 // The scale of scale byte `at` of a word, as the conversions take it: they read its exponent

@@ -678,7 +678,8 @@ reshard_status_t reshard_block_grad_workspace(const reshard_matrix_t* dy, const 
 reshard_status_t reshard_group_quantize(const reshard_matrix_t* src, const reshard_matrix_t* dst, void* stream);
 
 /* Write the values a group-scaled matrix stands for into the plain matrix dst of the
- * same shape, each rounded once (to nearest, ties to even; exact for F32 and BF16). */
+ * same shape, each rounded once (to nearest, ties to even; exact for F32 and BF16, past
+ * whose range it is infinite). */
 reshard_status_t reshard_group_dequantize(const reshard_matrix_t* src, const reshard_matrix_t* dst, void* stream);
 
 /*
@@ -741,8 +742,8 @@ reshard_status_t reshard_expert_gather(const reshard_matrix_t* x, const int32_t*
 /*
  * out[t, :] = sum over j of weights[t, j] * rows[position[t, j], :], over the choices
  * that have a row, in the order of j, products and sums in binary32 (fused or
- * rounded one after the other), rounded once.  A token without any gets zeros.  rows and out are plain, of one type and of
- * the same columns; weights is a plain matrix (tokens x choices, any type), or NULL
+ * rounded one after the other), rounded once.  A token without any gets zeros.  rows and
+ * out are plain, of one type and of the same columns; weights is a plain matrix (tokens x choices, any type), or NULL
  * for weights of 1 (out is then the gradient of reshard_expert_gather's x from that of
  * its rows).
  */
