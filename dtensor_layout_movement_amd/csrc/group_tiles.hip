@@ -80,8 +80,8 @@ __device__ __forceinline__ void make_tile(const Rows& a, const Weight& b, int gr
   };
 
   // Eight scale bytes of a row of the weight for its steps kb to kb + 2, whose first is at bit
-  // scales_at(kb): the row's last eight at most.  Past the last group any of the row's
-  // does: a is zero there.
+  // scales_at(kb): the row's last eight at most.  Past the last group the byte is 0 or 1 (the
+  // last one's top bit): what lies there, whatever it is, has to be finite, since a is zero.
   const uint8_t* scales = b.scales + row_b0 * b.scale_stride;
   const auto scales_at = [&](uint32_t kb) { return 8 * (int(kb) * 2 - min(int(kb) * 2, groups - 8)); };
   constexpr int kScaleRows = SHARED ? 1 : kN;
@@ -147,9 +147,10 @@ __device__ __forceinline__ void make_tile(const Rows& a, const Weight& b, int gr
   // `fill` asks for what comes later, behind the step's first reads; `turn`, between the
   // step's last read and its last products, waits for the next step's and reads its first.
   const auto step = [&](const uint8_t* tile, const uint64_t (&s)[kN], int bit, auto fill, auto turn) {
+    const int by = min(bit + 8 * (part >> 1), 63);
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      const float f = scale_of(uint32_t(s[i] >> ((bit + 8 * (part >> 1)) & 63)), 0);
+      const float f = scale_of(uint32_t(s[i] >> by), 0);
       w[i].half[0] = widen8_fp4(uint32_t(raw[i][0]), f);
       w[i].half[1] = widen8_fp4(uint32_t(raw[i][1]), f);
     }
