@@ -48,12 +48,18 @@ def build(verbose: bool = False) -> str:
         for src in SOURCES:
             obj = os.path.join(folder, os.path.basename(src) + ".o")
             jobs.append(([hipcc(), *HIP_FLAGS, "-c", "-I", INCLUDE, "-I", CSRC, src, "-o", obj], obj))
-        with ThreadPoolExecutor(min(8, int(os.environ.get("MAX_JOBS", 8)))) as pool:
+        with ThreadPoolExecutor(_jobs()) as pool:
             list(pool.map(lambda job: _run(job[0], verbose), jobs))
         tmp = LIB_PATH + ".tmp"
         _run([hipcc(), *HIP_FLAGS, "-shared", *[obj for _, obj in jobs], "-o", tmp], verbose)
     os.replace(tmp, LIB_PATH)
     return LIB_PATH
+
+
+def _jobs() -> int:
+    """Compilers at a time: eight, or fewer where MAX_JOBS is a number of them."""
+    given = os.environ.get("MAX_JOBS", "").strip()
+    return min(8, int(given) if given.isdecimal() and int(given) else 8)
 
 
 def _run(cmd, verbose) -> None:
