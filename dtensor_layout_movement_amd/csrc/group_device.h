@@ -76,7 +76,9 @@ __device__ __forceinline__ float scale_of(uint32_t word, int at) {
   return __builtin_bit_cast(float, exponent & 0x7f800000u);
 }
 
-// Eight 4-bit elements times a power of two as bfloat16: exact (two significant bits).
+// Eight 4-bit elements times a power of two as bfloat16: exact (two significant bits, from
+// 2^-128 on, a subnormal, which the matrix instructions take as it is), infinite where 4 or 6
+// is scaled by 2^126, or 2 and more by 2^127.
 __device__ __forceinline__ bf16x8 widen8_fp4(uint32_t q, float scale) {
   bf16x2 p[4];
   p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 0);

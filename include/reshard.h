@@ -661,8 +661,12 @@ reshard_status_t reshard_block_grad_workspace(const reshard_matrix_t* dy, const 
  *
  * What is said above of block-scaled calls (streams, capture, memory, overlaps,
  * matrices with no elements, fixed order of sums, errors) holds for the calls here
- * and for those of the experts below: each is one to three kernel launches (more
- * where the counts of pieces pass 2^31).
+ * and for those of the experts below: each is one to three kernel launches.  Calls that
+ * move or convert make more where one launch's 2^23 - 1 workgroups do not do (64 groups
+ * to quantize or 512 pieces of 16 bytes to read back make one; a token for the gradients;
+ * at most 8 KiB of a token to gather or combine).  A product that needs more than those
+ * is refused: 16 rows of one weight by 64 columns of out (32 with an F16 or F32 a) make at
+ * most one.
  */
 #define RESHARD_GROUP 32
 
@@ -672,7 +676,8 @@ reshard_status_t reshard_block_grad_workspace(const reshard_matrix_t* dy, const 
  * amax <= 6 * 2^e (0 for a group of zeros), its scale byte e + 127 and each element
  * x / 2^e rounded to nearest, ties to even.  The format has no infinity and no NaN:
  * a group with an element that is not finite gets the scale byte 255 and zeros, all
- * of it NaN.  Padding of the last group is written as zero; bytes beyond it, and
+ * of it NaN.  (Magnitudes of 3.5 * 2^126 and more, which round to 2^128, read back as
+ * infinities.)  Padding of the last group is written as zero; bytes beyond it, and
  * rows beyond the matrices', are left as they were.
  */
 reshard_status_t reshard_group_quantize(const reshard_matrix_t* src, const reshard_matrix_t* dst, void* stream);
@@ -687,9 +692,11 @@ reshard_status_t reshard_group_dequantize(const reshard_matrix_t* src, const res
  * by a group-scaled weight b stored output features first.  a is used unrounded: an
  * F16 or F32 value is cut into two or three bfloat16 parts that add up to it, each
  * multiplied exactly.  Sums are held in binary32 and rounded once to out's type,
- * which is plain and need not be a's (terms and parts that stay below 2^-126, where
- * the matrix instructions have no bits, may be lost).  An infinite element, or a sum
- * past binary32, gives an infinity or a NaN, as in floating point.
+ * which is plain and need not be a's (terms and parts of a that stay below 2^-126,
+ * where the matrix instructions have no bits, may be lost; smaller elements of b are
+ * not).  Elements of b past binary32's largest value (4 or 6 under the scale 2^126, 2 and
+ * more under 2^127) are infinite.  An infinite element, or a sum past binary32, gives an
+ * infinity or a NaN.
  * workspace: device memory of at least reshard_group_matmul_workspace bytes (0: may
  * be NULL), 16-byte aligned, not shared with a call that may run at the same time.
  * Its contents need no preparation.
