@@ -215,11 +215,12 @@ GroupPlan plan_group_matmul(const reshard_matrix_t& a, const reshard_matrix_t& b
   const int64_t stride = std::max(direct ? a.row_stride * 2 : parts * part_steps * 128, std::max(b.row_stride / 2, b.scale_stride));
   // (their rows are at most 2^22 bytes apart, a tile's within 32-bit offsets, and they load
   // eight scales of a row together)
-  // Which form, by the rows of a weight (us): up to 16, 16 x 14336 x 4096 11.4 with the form
-  // for few rows and 13.9 with tiles of 64; up to 64, 33 x 14336 x 4096 18.3 with those.  Larger
-  // tiles where they fill the card: 512 x 14336 x 4096 63 with 128 x 128, 73 with 64 x 128; 64
-  // experts' 9600 rows 417 and 450, their 4800 294 and 290; 4096 x 14336 x 4096 440 with 256 x
-  // 256, 64 experts' 16384 rows 603 and 645 with 128 x 128, their 4800 393 and 294.
+  // Which form, by the rows of a weight (us): a's rows over the experts, which is all that the
+  // host knows, and too many where some are no held expert's.  Up to 16, 16 x 14336 x 4096 11.4
+  // with the form for few rows and 13.9 with tiles of 64; up to 64, 33 x 14336 x 4096 18.3 with
+  // those.  Larger tiles where they fill the card: 512 x 14336 x 4096 63 with 128 x 128, 73 with
+  // 64 x 128; 64 experts' 9600 rows 417 and 450, their 4800 294 and 290; 4096 x 14336 x 4096 445
+  // with 256 x 256, 64 experts' 16384 rows 603 and 645 with 128 x 128, their 4800 393 and 294.
   const int64_t mean = experts ? a.rows / experts : a.rows;
   if (mean > kRowsHeight && groups_of(a.cols) >= 8 && out.cols && stride <= (int64_t(1) << 22)) {
     if (tiles(256, 256) >= 192 && out.cols > 128 && (!experts || mean >= 192)) {

@@ -34,9 +34,9 @@ constexpr int kRowA = kStep * 2, kRowB = kThree * kStep / 2;  // bytes of a row 
 // read another row cost the first cache a line each).  In tiles of 256 rows, whose registers
 // are full, by every lane that uses them.
 //
-// 256 x 256 tiles: 4096 x 14336 x 4096 takes 440 us (1090 TFLOP/s; the library's product of
-// bfloat16 matrices 406), with an MFMA pipe that is busy for 45% of the time; without the
-// loads it would take 382, without the conversions 435.  128 x 128, two workgroups a CU:
+// 256 x 256 tiles: 4096 x 14336 x 4096 takes 445 us (1080 TFLOP/s; the library's product of
+// bfloat16 matrices 406), with an MFMA pipe that is busy for 45% of the time; of 440, 382 were
+// left without the loads and 435 without the conversions.  128 x 128, two workgroups a CU:
 // 512 x 14336 x 4096 63 us.  64 x 128: 33 x 4096 x 14336 14 us and 4 for the join.
 template <int DT, int BM, int BN, int WM, int WN, bool SHARED>
 __device__ __forceinline__ void make_tile(const Rows& a, const Weight& b, int groups, const Chunk& c, int n0,

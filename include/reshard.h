@@ -776,8 +776,11 @@ reshard_status_t reshard_expert_combine_grad(const reshard_matrix_t* dout, const
  * offsets[e + 1], is row r of a times expert e's weight.  b holds the experts' weights one
  * below the other (experts * n rows, n the columns of out).  offsets is as
  * reshard_expert_sort writes it: increasing.  Rows of out that no expert has are left as
- * they were, and those of a are not used.  Everything else is as for
- * reshard_group_matmul.
+ * they were, and those of a are not used.  The kernel, its workspace and its launch are
+ * chosen by the rows of a, all of which count: where experts have far fewer (a rank that
+ * holds some of the experts and a row for every choice), matrices described with a known
+ * bound of the rows that they have are faster and need less workspace.  Everything else
+ * is as for reshard_group_matmul.
  */
 reshard_status_t reshard_expert_matmul(const reshard_matrix_t* a, const reshard_matrix_t* b, const int32_t* offsets,
                                        int64_t experts, const reshard_matrix_t* out, void* workspace,
